@@ -326,6 +326,148 @@ int misa_decode_score_topk(const uint16_t* Q, const float* w, const int32_t* hea
                            int h, int k, int32_t* idx, float* logits, int64_t ld, void* stream);
 
 /*
+ * Bookkeeping of one serving step, on the device.  n_seq requests add
+ * q_lens[b] >= 0 new tokens to the ctx_lens[b] >= 0 that their caches hold; the
+ * new tokens of all requests are packed in request order (row t of every [n_tok]
+ * buffer).  One launch gives, for the append, the indexer and the attention calls:
+ *   cu_q      [n_seq + 1]  rows before each request; cu_q[n_seq] = rows in all
+ *   seq_lens  [n_seq]      ctx_lens + q_lens (may be the ctx_lens array itself)
+ *   positions [n_tok]      position of each row in its sequence
+ *   slots     [n_tok]      cache row of each row: page * page_size + row in page
+ *   seq_of    [n_tok]      request of each row
+ *   granted   [n_seq]      1, or 0 for a request that was refused
+ * Rows past cu_q[n_seq] (a padded batch) get -1 in positions, slots and seq_of.
+ * New pages are taken from the top of the stack free_pages[0 .. *free_count):
+ * page i of the step is free_pages[*free_count - 1 - i], in request order, and
+ * goes to the next entry of the request's block_tables row ([n_seq, max_blocks]);
+ * *free_count_out (may be free_count) gets the pages left.  With free_pages ==
+ * NULL the tables are complete already and only the maps are built.
+ * A request is refused, with seq_lens 0, -1 in its rows and no page taken, when
+ * its tokens pass max_blocks pages or n_tok rows, when a length is negative, or
+ * when the pool runs out (then every later request that needs a page is refused
+ * too); it is reported as MISA_ERR_DEVICE, as is a page id outside 0..n_pages-1
+ * (slot -1).  Updating lengths and count in place lets a captured decode step
+ * advance by itself.  n_seq <= 8192, page_size 16, 32, 64 or 128 (else
+ * MISA_ERR_UNSUPPORTED); n_pages * page_size < 2^31; 0 <= free_cap entries in
+ * free_pages.  No other two buffers may overlap.
+ */
+int misa_plan_step(const int32_t* q_lens, const int32_t* ctx_lens, int n_seq, int32_t* block_tables,
+                   int max_blocks, int page_size, int64_t n_pages, int n_tok,
+                   const int32_t* free_pages, int64_t free_cap, const int32_t* free_count,
+                   int32_t* cu_q, int32_t* seq_lens, int32_t* positions, int32_t* slots,
+                   int32_t* seq_of, int32_t* granted, int32_t* free_count_out, void* stream);
+/* Gives back the pages of every request with release[b] != 0: the
+ * ceil(seq_lens[b] / page_size) pages of its table row are pushed onto the stack
+ * in request order, seq_lens[b] becomes 0 and *free_count grows.  Pages that the
+ * stack (free_cap entries) cannot hold are dropped and reported as
+ * MISA_ERR_DEVICE.  Other limits as misa_plan_step. */
+int misa_release_pages(const int32_t* release, int32_t* seq_lens, const int32_t* block_tables,
+                       int n_seq, int max_blocks, int page_size, int64_t n_pages,
+                       int32_t* free_pages, int64_t free_cap, int32_t* free_count, void* stream);
+
+/*
+ * Rotary positions.  Elements [offset, offset + rope_dim) of a head row of d are
+ * turned in pairs, pair i < rope_dim / 2 by the angle phi = position * inv_freq[i]:
+ *   (a, b) -> amplitude * (a cos phi - b sin phi, a sin phi + b cos phi)
+ * a, b are elements 2i, 2i + 1 of the part (interleaved != 0) or i, i +
+ * rope_dim / 2; the other elements of the row are kept.  Angles are formed and
+ * reduced in 64 bits, the rotation in 32, each result rounded once.
+ *   X [n, H, d] bf16 codes, positions [n] int32, inv_freq [rope_dim / 2] fp64
+ *   (device memory), d in {32, 64, 128}, rope_dim a multiple of 16, offset of 8
+ *   (else MISA_ERR_UNSUPPORTED), offset + rope_dim <= d; X and the results
+ *   16-byte aligned, inv_freq 8-byte aligned.
+ * misa_rope writes Y [n, H, d] bf16 (Y may be X); transpose != 0 applies the
+ * transposed rotation (phi negated): the gradient of X from that of Y.
+ * misa_rope_fp8 writes e4m3 codes Y8 [n, H, d] and a scale per row y_scale
+ * [n, H] = max |row| / 448 (1 where that is 0), codes = e4m3(row / scale): the
+ * operands of misa_score_tokens_fp8.  A row that is not finite is reported as
+ * MISA_ERR_DEVICE.  Rows with a negative position are left as they were.
+ */
+int misa_rope(const uint16_t* X, const int32_t* positions, const double* inv_freq, int n, int H,
+              int d, int rope_dim, int offset, int interleaved, float amplitude, int transpose,
+              uint16_t* Y, void* stream);
+int misa_rope_fp8(const uint16_t* X, const int32_t* positions, const double* inv_freq, int n, int H,
+                  int d, int rope_dim, int offset, int interleaved, float amplitude, uint8_t* Y8,
+                  float* y_scale, void* stream);
+/* Rotates the key rows K [n, H, d] as misa_rope does and writes row t to row
+ * slots[t] of a paged cache k_pages [n_pages, page_size, H, d]: bf16 codes
+ * (kdtype MISA_K_BF16), or e4m3 codes with k_scale [n_pages, page_size, H]
+ * (MISA_K_FP8E4M3).  H = 1 writes the index-key caches that the _paged and
+ * decode calls read.  V and v_pages (both or neither; bf16, same shapes) are
+ * copied beside them, unrotated.  Rows with a negative slot are skipped; a slot
+ * past the pool is skipped and reported as MISA_ERR_DEVICE; slots must be
+ * distinct. */
+int misa_cache_append(const uint16_t* K, const uint16_t* V, const int32_t* positions,
+                      const int32_t* slots, const double* inv_freq, int n, int H, int d,
+                      int rope_dim, int offset, int interleaved, float amplitude, int kdtype,
+                      void* k_pages, float* k_scale, uint16_t* v_pages, int page_size,
+                      int64_t n_pages, void* stream);
+
+/* How misa_rope_frequencies adapts the frequencies base^(-2i / rope_dim) to
+ * contexts `factor` times longer than the trained length. */
+typedef enum misa_rope_scaling {
+    MISA_ROPE_PLAIN = 0,
+    MISA_ROPE_LINEAR = 1, /* every frequency divided by factor (position interpolation) */
+    MISA_ROPE_BASE = 2,   /* base * factor^(rope_dim / (rope_dim - 2)): the slowest pair is
+                             slowed by factor, the fastest kept (NTK-aware scaling) */
+    MISA_ROPE_BANDS = 3   /* pairs with more than fast_turns turns within trained_len kept, those
+                             with fewer than slow_turns divided by factor, a linear blend over
+                             the pair index between (whole indices, rounded outwards); amplitude
+                             0.1 ln(factor) + 1 (YaRN) */
+} misa_rope_scaling;
+/* Host function: fills inv_freq [rope_dim / 2] and *amplitude, both HOST memory.
+ * rope_dim even, 2..1024; base > 1; factor >= 1 unless MISA_ROPE_PLAIN;
+ * trained_len, fast_turns > slow_turns > 0 for MISA_ROPE_BANDS only. */
+int misa_rope_frequencies(int rope_dim, double base, int scaling, double factor, double trained_len,
+                          double fast_turns, double slow_turns, double* inv_freq,
+                          double* amplitude);
+
+/*
+ * Attention of new tokens over paged caches.  Row t of the packed batch belongs
+ * to sequence b with cu_q[b] <= t < cu_q[b + 1]; its n_b = cu_q[b + 1] - cu_q[b]
+ * new tokens are the last n_b of the sequence's seq_lens[b] keys (already in the
+ * cache), so row t sits at position p = seq_lens[b] - n_b + t - cu_q[b] and sees
+ * the keys s <= p; with window > 0 only those with s > p - window or s < sinks.
+ *   out[t, h] = sum_s softmax_s(scale * Q[t, h] . K[s, h / G]) V[s, h / G],  G = H / H_kv
+ *   lse[t, h] = log sum_s exp(scale * Q[t, h] . K[s, h / G])   (nullable, fp32)
+ *   Q, out [n_tok, H, d] bf16; k_pages, v_pages [n_pages, page_size, H_kv, d] bf16;
+ *   block_tables [n_seq, max_blocks], cu_q [n_seq + 1], seq_lens [n_seq] int32
+ *   (device); d in {64, 128}, H_kv divides H, G <= 128, page_size 16, 32, 64 or
+ *   128 (else MISA_ERR_UNSUPPORTED); scale > 0; sinks need a window.
+ * One call serves prefill chunks, single new tokens and mixed batches; rows past
+ * cu_q[n_seq] are left as they were.  A row that sees nothing gives zeros and an
+ * lse of -inf.  Products take bf16 operands with fp32 sums; the weights are
+ * rounded to bf16 for the second product, their sum is not.  Cache rows at or
+ * past seq_lens[b] may hold anything; rows below it must be finite (a
+ * non-finite value there may reach every row of its 128-key tile).  A length
+ * past max_blocks * page_size is reported as MISA_ERR_DEVICE and clamped; a
+ * table entry outside 0..n_pages-1 is reported and read as page 0.  Results do
+ * not depend on timing.
+ * ws: misa_workspace_size("attend", 1, 0, d, 0) bytes, 16-byte aligned, its
+ * contents need no initialisation and are unspecified afterwards; calls that
+ * may overlap on the GPU need a workspace each.
+ */
+int misa_attend_paged(const uint16_t* Q, const uint16_t* k_pages, const uint16_t* v_pages,
+                      const int32_t* block_tables, int max_blocks, int page_size, int64_t n_pages,
+                      const int32_t* cu_q, const int32_t* seq_lens, int n_seq, int n_tok, int H,
+                      int H_kv, int d, float scale, int window, int sinks, uint16_t* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream);
+/* Attention of each row over its own list of tokens, as misa_score_topk,
+ * misa_rerank and misa_decode_score_topk give them: the sum runs over the
+ * entries of idx[t, 0..k) with 0 <= idx[t, i] <= positions[t], in any order (an
+ * entry listed twice counts twice; the others are ignored).  seq_of [n_tok] is
+ * the sequence of each row (the block table it reads), positions [n_tok] its
+ * position; rows with seq_of < 0 are left as they were, seq_of >= n_seq and
+ * tokens past max_blocks * page_size are skipped and reported as
+ * MISA_ERR_DEVICE.  1 <= k <= 16384; the rest, and ws, as misa_attend_paged. */
+int misa_attend_selected(const uint16_t* Q, const uint16_t* k_pages, const uint16_t* v_pages,
+                         const int32_t* block_tables, int max_blocks, int page_size,
+                         int64_t n_pages, const int32_t* seq_of, const int32_t* positions,
+                         const int32_t* idx, int k, int n_seq, int n_tok, int H, int H_kv, int d,
+                         float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
  * Stage timing of misa_score_topk (diagnostic; not a step of the method).
  * Between misa_profile_start() and misa_profile_stop(), each launch of the fused
  * sequence is bracketed by CUDA events on the call's stream.  misa_profile_stop
@@ -340,7 +482,8 @@ int misa_profile_stop(double* ms, int* counts, int n);
 const char* misa_profile_stage_name(int i);
 
 /* Workspace bytes needed by op "topk", "rerank" or "score_topk" for the given
- * sizes (0 if none). */
+ * sizes (0 if none), or by the attention calls on the current device (op
+ * "attend": n_q any positive number, k the head size d, n_k and kp unused). */
 size_t misa_workspace_size(const char* op, int n_q, int64_t n_k, int k, int kp);
 
 /* Static text for a misa_status value. */

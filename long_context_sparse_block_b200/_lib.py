@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -25,6 +26,7 @@ MISA_ERR_DEVICE = -6
 MISA_K_BF16 = 0
 MISA_K_FP8E4M3 = 1
 MISA_K_BF16_SCALED = 2
+MISA_ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "bands": 3}
 
 
 class MisaError(RuntimeError):
@@ -34,6 +36,7 @@ class MisaError(RuntimeError):
 
 
 _vp, _i64, _int, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 _SIGS = {
     "misa_pool_keys": (_int, [_vp, _vp, _int, _i64, _int, _int, _vp, _vp, _vp]),
     "misa_pool_keys_range": (_int, [_vp, _vp, _int, _i64, _int, _int, _i64, _i64, _vp, _vp, _vp]),
@@ -65,6 +68,19 @@ _SIGS = {
                                        _vp, _vp]),
     "misa_decode_score_topk": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _vp, _int, _int, _i64, _vp,
                                       _int, _int, _int, _int, _int, _vp, _vp, _i64, _vp]),
+    "misa_plan_step": (_int, [_vp, _vp, _int, _vp, _int, _int, _i64, _int, _vp, _i64, _vp, _vp, _vp,
+                              _vp, _vp, _vp, _vp, _vp, _vp]),
+    "misa_release_pages": (_int, [_vp, _vp, _vp, _int, _int, _int, _i64, _vp, _i64, _vp, _vp]),
+    "misa_rope_frequencies": (_int, [_int, _f64, _int, _f64, _f64, _f64, _f64, _vp, _vp]),
+    "misa_rope": (_int, [_vp, _vp, _vp, _int, _int, _int, _int, _int, _int, _f32, _int, _vp, _vp]),
+    "misa_rope_fp8": (_int, [_vp, _vp, _vp, _int, _int, _int, _int, _int, _int, _f32, _vp, _vp,
+                             _vp]),
+    "misa_cache_append": (_int, [_vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _int, _int, _f32,
+                                 _int, _vp, _vp, _vp, _int, _i64, _vp]),
+    "misa_attend_paged": (_int, [_vp, _vp, _vp, _vp, _int, _int, _i64, _vp, _vp, _int, _int, _int,
+                                 _int, _int, _f32, _int, _int, _vp, _vp, _vp, _sz, _vp]),
+    "misa_attend_selected": (_int, [_vp, _vp, _vp, _vp, _int, _int, _i64, _vp, _vp, _vp, _int, _int,
+                                    _int, _int, _int, _int, _f32, _vp, _vp, _vp, _sz, _vp]),
     "misa_profile_start": (_int, []),
     "misa_profile_stop": (_int, [_vp, _vp, _int]),
     "misa_profile_stage_name": (ctypes.c_char_p, [_int]),
@@ -503,6 +519,279 @@ def misa_decode_score_topk(Q, w, heads, pages, block_tables, seq_lens, k: int, k
                                      ctypes.c_void_p(logits.data_ptr()), logits.stride(0), _stream())
     _check("misa_decode_score_topk", st)
     return idx, logits
+
+
+# ---------------------------------------------------------------- serving steps
+
+_I32 = (torch.int32,)
+_F32 = (torch.float32,)
+
+
+def _arg(t, n: int, dtypes, name: str, dev: int):
+    """Address of `t`, which must hold at least `n` contiguous elements of one of
+    `dtypes` on device `dev` (the C ABI sees the address only)."""
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, the call needs {n}")
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, the other tensors on cuda:{dev}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(dev: int) -> int:
+    """The current stream of device `dev`, which must be the current device."""
+    if torch.cuda.current_device() != dev:
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+class StepPlan(NamedTuple):
+    """The maps of one serving step (misa_plan_step), all int32 device tensors."""
+    cu_q: torch.Tensor        # [n_seq + 1] rows before each request
+    seq_lens: torch.Tensor    # [n_seq] keys of each request, its new tokens among them
+    positions: torch.Tensor   # [n_tok] position of each row in its sequence (-1: no row)
+    slots: torch.Tensor       # [n_tok] cache row of each row (-1: none)
+    seq_of: torch.Tensor      # [n_tok] request of each row (-1: none)
+    granted: torch.Tensor     # [n_seq] 1, or 0: refused
+
+
+def misa_plan_step(q_lens, ctx_lens, block_tables, page_size: int, n_tok: int | None = None,
+                   n_pages: int | None = None, free_pages=None, free_count=None,
+                   free_count_out=None, cu_q=None, seq_lens=None, positions=None, slots=None,
+                   seq_of=None, granted=None) -> StepPlan:
+    """Block tables and maps of one step from the request lengths, on the device.
+
+    q_lens, ctx_lens [n_seq] int32: new and earlier tokens of each request;
+    block_tables [n_seq, max_blocks] int32, extended in place with pages from the
+    stack free_pages[:free_count] (both None: the tables are complete).  n_tok
+    rows of the packed batch (default: the size of `positions`); n_pages bounds
+    the page ids (default: any whose rows are int32).  free_count_out (default
+    free_count itself) gets the pages left; seq_lens may be ctx_lens."""
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [n_seq, max_blocks]")
+    n_seq, max_blocks = block_tables.shape
+    if n_tok is None:
+        if positions is None:
+            raise ValueError("give n_tok, or the positions buffer")
+        n_tok = positions.numel()
+    dev = block_tables.get_device()
+    i32 = dict(dtype=torch.int32, device=block_tables.device)
+    if cu_q is None:
+        cu_q = torch.empty(n_seq + 1, **i32)
+    if seq_lens is None:
+        seq_lens = torch.empty(n_seq, **i32)
+    if positions is None:
+        positions = torch.empty(n_tok, **i32)
+    if slots is None:
+        slots = torch.empty(n_tok, **i32)
+    if seq_of is None:
+        seq_of = torch.empty(n_tok, **i32)
+    if granted is None:
+        granted = torch.empty(n_seq, **i32)
+    if (free_pages is None) != (free_count is None):
+        raise ValueError("free_pages and free_count go together")
+    if n_pages is None:
+        n_pages = 0x7fffffff // max(1, page_size)
+    fp = fc = fo = None
+    cap = 0
+    if free_pages is not None:
+        cap = free_pages.numel()
+        fp = _arg(free_pages, 0, _I32, "free_pages", dev)
+        fc = _arg(free_count, 1, _I32, "free_count", dev)
+        fo = fc if free_count_out is None else _arg(free_count_out, 1, _I32, "free_count_out", dev)
+    st = _lib.misa_plan_step(
+        _arg(q_lens, n_seq, _I32, "q_lens", dev), _arg(ctx_lens, n_seq, _I32, "ctx_lens", dev), n_seq,
+        _arg(block_tables, 0, _I32, "block_tables", dev), max_blocks, page_size, n_pages, n_tok, fp,
+        cap, fc, _arg(cu_q, n_seq + 1, _I32, "cu_q", dev), _arg(seq_lens, n_seq, _I32, "seq_lens", dev),
+        _arg(positions, n_tok, _I32, "positions", dev), _arg(slots, n_tok, _I32, "slots", dev),
+        _arg(seq_of, n_tok, _I32, "seq_of", dev), _arg(granted, n_seq, _I32, "granted", dev), fo,
+        _raw_stream(dev))
+    _check("misa_plan_step", st)
+    return StepPlan(cu_q, seq_lens, positions, slots, seq_of, granted)
+
+
+def misa_release_pages(release, seq_lens, block_tables, page_size: int, free_pages, free_count,
+                       n_pages: int | None = None) -> None:
+    """Pushes the pages of every request with release[b] != 0 onto the stack
+    free_pages[:free_count] and sets its length to zero, in place."""
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [n_seq, max_blocks]")
+    n_seq, max_blocks = block_tables.shape
+    dev = block_tables.get_device()
+    if n_pages is None:
+        n_pages = 0x7fffffff // max(1, page_size)
+    st = _lib.misa_release_pages(
+        _arg(release, n_seq, _I32, "release", dev), _arg(seq_lens, n_seq, _I32, "seq_lens", dev),
+        _arg(block_tables, 0, _I32, "block_tables", dev), n_seq, max_blocks, page_size, n_pages,
+        _arg(free_pages, 0, _I32, "free_pages", dev), free_pages.numel(),
+        _arg(free_count, 1, _I32, "free_count", dev), _raw_stream(dev))
+    _check("misa_release_pages", st)
+
+
+def misa_rope_frequencies(rope_dim: int, base: float = 10000.0, scaling: str = "plain",
+                          factor: float = 1.0, trained_len: float = 4096.0,
+                          fast_turns: float = 32.0, slow_turns: float = 1.0, device="cuda"):
+    """Angles per position of the rope_dim / 2 pairs (fp64 tensor on `device`) and the
+    amplitude of the rotation.  scaling: "plain", "linear", "base" or "bands"."""
+    if scaling not in MISA_ROPE_SCALING:
+        raise ValueError(f"scaling {scaling!r}: one of {tuple(MISA_ROPE_SCALING)}")
+    buf = (ctypes.c_double * max(1, rope_dim // 2))()
+    amp = ctypes.c_double()
+    st = _lib.misa_rope_frequencies(rope_dim, base, MISA_ROPE_SCALING[scaling], factor, trained_len,
+                                    fast_turns, slow_turns, buf, ctypes.byref(amp))
+    _check("misa_rope_frequencies", st)
+    return torch.tensor(list(buf), dtype=torch.float64).to(device), amp.value
+
+
+def _rope_args(x, positions, inv_freq, offset, interleaved, amplitude, dev, d):
+    n, H = x.shape[0], x.shape[1] if x.dim() == 3 else 1
+    return (_arg(x, 0, _BF16_CODES, "x", dev), _arg(positions, n, _I32, "positions", dev),
+            _arg(inv_freq, 0, (torch.float64,), "inv_freq", dev), n, H, d, 2 * inv_freq.numel(),
+            offset, int(bool(interleaved)), amplitude)
+
+
+def misa_rope(x, positions, inv_freq, offset: int = 0, interleaved: bool = False,
+              amplitude: float = 1.0, transpose: bool = False, out=None):
+    """Head rows x [n, H, d] bf16 with elements [offset, offset + 2 len(inv_freq)) rotated by
+    positions [n] -> out (a new tensor, or `out`, which may be x).  transpose: the
+    transposed rotation, which takes the gradient of the result to that of x."""
+    if x.dim() != 3:
+        raise ValueError("x must be [n, H, d]")
+    dev, d = x.get_device(), x.shape[2]
+    if out is None:
+        out = torch.empty_like(x)
+    a = _rope_args(x, positions, inv_freq, offset, interleaved, amplitude, dev, d)
+    st = _lib.misa_rope(*a, int(bool(transpose)), _arg(out, x.numel(), _BF16_CODES, "out", dev),
+                        _raw_stream(dev))
+    _check("misa_rope", st)
+    return out
+
+
+def misa_rope_fp8(x, positions, inv_freq, offset: int = 0, interleaved: bool = False,
+                  amplitude: float = 1.0, codes=None, scale=None):
+    """misa_rope with e4m3 results: (codes [n, H, d] uint8, scale [n, H] fp32), the queries
+    of misa_score_tokens_fp8."""
+    if x.dim() != 3:
+        raise ValueError("x must be [n, H, d]")
+    dev, (n, H, d) = x.get_device(), x.shape
+    if codes is None:
+        codes = torch.empty((n, H, d), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((n, H), dtype=torch.float32, device=x.device)
+    a = _rope_args(x, positions, inv_freq, offset, interleaved, amplitude, dev, d)
+    st = _lib.misa_rope_fp8(*a, _arg(codes, n * H * d, _E4M3_CODES, "codes", dev),
+                            _arg(scale, n * H, _F32, "scale", dev), _raw_stream(dev))
+    _check("misa_rope_fp8", st)
+    return codes, scale
+
+
+def misa_cache_append(k, positions, slots, inv_freq, k_pages, k_scale=None, v=None, v_pages=None,
+                      offset: int = 0, interleaved: bool = False, amplitude: float = 1.0) -> None:
+    """Rotates key rows k [n, H, d] (or [n, d]) and writes row t to cache row slots[t] of
+    k_pages [n_pages, page_size, H, d] (or [n_pages, page_size, d]): bf16, or e4m3 with
+    k_scale [n_pages, page_size(, H)].  Values v are copied into v_pages beside them."""
+    if k.dim() not in (2, 3) or k_pages.dim() != k.dim() + 1 or k_pages.shape[2:] != k.shape[1:]:
+        raise ValueError("k [n, H, d] with k_pages [n_pages, page_size, H, d], or [n, d] with "
+                         "[n_pages, page_size, d]")
+    dev, d = k.get_device(), k.shape[-1]
+    n_pages, page_size = k_pages.shape[:2]
+    kd = _kdtype(k_pages)
+    if (v is None) != (v_pages is None):
+        raise ValueError("v and v_pages go together")
+    rows = n_pages * page_size * (k.shape[1] if k.dim() == 3 else 1)
+    pv = pvp = None
+    if v is not None:
+        pv = _arg(v, k.numel(), _BF16_CODES, "v", dev)
+        pvp = _arg(v_pages, rows * d, _BF16_CODES, "v_pages", dev)
+    if kd == MISA_K_FP8E4M3 and k_scale is None:
+        raise ValueError("e4m3 pages need k_scale")
+    a = _rope_args(k, positions, inv_freq, offset, interleaved, amplitude, dev, d)
+    st = _lib.misa_cache_append(
+        a[0], pv, a[1], _arg(slots, k.shape[0], _I32, "slots", dev), *a[2:], kd,
+        _arg(k_pages, 0, _BF16_CODES + _E4M3_CODES, "k_pages", dev),
+        None if k_scale is None else _arg(k_scale, rows, _F32, "k_scale", dev), pvp, page_size,
+        n_pages, _raw_stream(dev))
+    _check("misa_cache_append", st)
+
+
+def _attend_args(Q, k_pages, v_pages, block_tables, scale, out, want_lse, lse, ws):
+    """What the two attention calls share, checked: addresses, sizes, results, workspace."""
+    if Q.dim() != 3 or k_pages.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("Q [n_tok, H, d], pages [n_pages, page_size, H_kv, d] and "
+                         "block_tables [n_seq, max_blocks]")
+    n_tok, H, d = Q.shape
+    n_pages, page_size, Hkv, dk = k_pages.shape
+    if dk != d or v_pages.shape != k_pages.shape:
+        raise ValueError(f"pages {tuple(k_pages.shape)} and {tuple(v_pages.shape)} do not match "
+                         f"heads of {d}")
+    n_seq, max_blocks = block_tables.shape
+    dev = Q.get_device()
+    if out is None:
+        out = torch.empty_like(Q)
+    if lse is None and want_lse:
+        lse = torch.empty((n_tok, H), dtype=torch.float32, device=Q.device)
+    pages = (_arg(Q, 0, _BF16_CODES, "Q", dev), _arg(k_pages, 0, _BF16_CODES, "k_pages", dev),
+             _arg(v_pages, 0, _BF16_CODES, "v_pages", dev),
+             _arg(block_tables, 0, _I32, "block_tables", dev), max_blocks, page_size, n_pages)
+    results = (_arg(out, n_tok * H * d, _BF16_CODES, "out", dev),
+               None if lse is None else _arg(lse, n_tok * H, _F32, "lse", dev))
+    stream = _raw_stream(dev)
+    ws_bytes = _lib.misa_workspace_size(b"attend", 1, 0, d, 0)
+    if ws is None:
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=Q.device)
+    elif ws.numel() * ws.element_size() < ws_bytes:
+        raise ValueError(f"ws holds {ws.numel() * ws.element_size()} bytes, the call needs {ws_bytes}")
+    work = (_arg(ws, 0, (ws.dtype,), "ws", dev), ws.numel() * ws.element_size(), stream)
+    if scale is None:
+        scale = d ** -0.5
+    return pages, (n_seq, n_tok, H, Hkv, d, scale), results, work, out, lse, dev
+
+
+def misa_attend_paged(Q, k_pages, v_pages, block_tables, cu_q, seq_lens, scale: float | None = None,
+                      window: int = 0, sinks: int = 0, out=None, lse=None, want_lse: bool = False,
+                      ws=None):
+    """Attention of the packed new tokens Q [n_tok, H, d] bf16 over paged caches k_pages,
+    v_pages [n_pages, page_size, H_kv, d] -> (out [n_tok, H, d], lse [n_tok, H] fp32 or None).
+
+    cu_q [n_seq + 1], seq_lens [n_seq] as misa_plan_step gives them: a sequence's new
+    tokens are the last of its keys.  scale defaults to d ** -0.5; window > 0 hides keys
+    at or past that distance except the first `sinks`.  Rows past cu_q[-1] are left as
+    they were.  ws: misa_workspace_size("attend", 1, 0, d, 0) bytes, allocated when None."""
+    pages, sizes, results, work, out, lse, dev = _attend_args(Q, k_pages, v_pages, block_tables,
+                                                              scale, out, want_lse, lse, ws)
+    n_seq, n_tok, H, Hkv, d, scale = sizes
+    st = _lib.misa_attend_paged(*pages, _arg(cu_q, n_seq + 1, _I32, "cu_q", dev),
+                                _arg(seq_lens, n_seq, _I32, "seq_lens", dev), n_seq, n_tok, H, Hkv, d,
+                                scale, window, sinks, *results, *work)
+    _check("misa_attend_paged", st)
+    return out, lse
+
+
+def misa_attend_selected(Q, k_pages, v_pages, block_tables, seq_of, positions, idx,
+                         scale: float | None = None, out=None, lse=None, want_lse: bool = False,
+                         ws=None):
+    """Attention of every row of Q [n_tok, H, d] over its own tokens idx [n_tok, k] int32
+    (the indexer's selection: -1 and tokens past positions[t] are ignored) in the cache of
+    sequence seq_of[t] -> (out, lse or None).  The rest as misa_attend_paged."""
+    if idx.dim() != 2:
+        raise ValueError("idx must be [n_tok, k]")
+    pages, sizes, results, work, out, lse, dev = _attend_args(Q, k_pages, v_pages, block_tables,
+                                                              scale, out, want_lse, lse, ws)
+    n_seq, n_tok, H, Hkv, d, scale = sizes
+    k = idx.shape[1]
+    st = _lib.misa_attend_selected(*pages, _arg(seq_of, n_tok, _I32, "seq_of", dev),
+                                   _arg(positions, n_tok, _I32, "positions", dev),
+                                   _arg(idx, n_tok * k, _I32, "idx", dev), k, n_seq, n_tok, H, Hkv, d,
+                                   scale, *results, *work)
+    _check("misa_attend_selected", st)
+    return out, lse
 
 
 def misa_profile_start() -> None:

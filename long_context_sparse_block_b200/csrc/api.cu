@@ -3,6 +3,7 @@
 // the stage launches.  Nothing here allocates device memory.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -81,6 +82,13 @@ struct KeyArg {
   bool fp8() const { return kdtype == MISA_K_FP8E4M3; }
 };
 
+// log2 of a supported page size (16, 32, 64 or 128), else -1.
+int page_shift_of(int page_size) {
+  for (int sh = 4; sh <= 7; ++sh)
+    if (page_size == (1 << sh)) return sh;
+  return -1;
+}
+
 KeyArg contiguous_keys(const void* K, const float* k_scale, int kdtype) {
   return KeyArg{K, k_scale, kdtype, KeyPages{nullptr, 0, 0}};
 }
@@ -89,10 +97,7 @@ KeyArg contiguous_keys(const void* K, const float* k_scale, int kdtype) {
 // unsupported size leaves page_shift at -1 for check_keys to refuse.
 KeyArg paged_keys(const void* pages, const float* k_scale, int kdtype, const int32_t* block_table,
                   int page_size, int64_t n_pages) {
-  int shift = -1;
-  for (int sh = 4; sh <= 7; ++sh)
-    if (page_size == (1 << sh)) shift = sh;
-  return KeyArg{pages, k_scale, kdtype, KeyPages{block_table, shift, n_pages}};
+  return KeyArg{pages, k_scale, kdtype, KeyPages{block_table, page_shift_of(page_size), n_pages}};
 }
 
 // scaled_bf16_ok: the call takes MISA_K_BF16_SCALED (contiguous keys only).
@@ -108,6 +113,77 @@ int check_keys(const KeyArg& k, int64_t n_k, bool scaled_bf16_ok = false) {
     if (k.kpg.n_pages < 1 || (k.kpg.n_pages << k.kpg.page_shift) > 0x7fffffffLL)
       return MISA_ERR_INVALID_ARG;
   }
+  return MISA_OK;
+}
+
+// The arguments that the rotary calls share.
+int check_rope(const uint16_t* X, const int32_t* positions, const double* inv_freq, int n, int H,
+               int d, int rope_dim, int offset, int interleaved, float amplitude) {
+  if (!X || !aligned16(X) || !positions || !aligned4(positions) || !inv_freq ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 7u) || n < 0 || H < 1 || rope_dim < 1 || offset < 0 ||
+      (interleaved != 0 && interleaved != 1) || !std::isfinite(amplitude))
+    return MISA_ERR_INVALID_ARG;
+  if (!good_d(d) || rope_dim % 16 != 0 || offset % 8 != 0) return MISA_ERR_UNSUPPORTED;
+  if (offset + static_cast<int64_t>(rope_dim) > d) return MISA_ERR_INVALID_ARG;
+  if (H > 65535) return MISA_ERR_UNSUPPORTED;
+  return MISA_OK;
+}
+
+// Angles per position of each pair (64 bits) and the amplitude of the rotation.
+void rope_frequencies(int r, double base, int scaling, double factor, double trained, double fast,
+                      double slow, double* inv_freq, double* amplitude) {
+  const double pi2 = 6.283185307179586476925;
+  *amplitude = 1.0;
+  if (scaling == MISA_ROPE_BASE) base *= std::pow(factor, static_cast<double>(r) / (r - 2));
+  // pair index (not whole) that makes `turns` turns within the trained length
+  auto pair_of = [&](double turns) { return r * std::log(trained / (turns * pi2)) / (2.0 * std::log(base)); };
+  double lo = 0.0, hi = 0.0;
+  if (scaling == MISA_ROPE_BANDS) {
+    lo = std::max(0.0, std::floor(pair_of(fast)));
+    hi = std::min(r - 1.0, std::ceil(pair_of(slow)));
+    *amplitude = 0.1 * std::log(factor) + 1.0;
+  }
+  for (int i = 0; i < r / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / r);
+    if (scaling == MISA_ROPE_LINEAR) {
+      inv_freq[i] = f / factor;
+    } else if (scaling == MISA_ROPE_BANDS) {
+      const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+      inv_freq[i] = f / factor * ramp + f * (1.0 - ramp);
+    } else {
+      inv_freq[i] = f;
+    }
+  }
+}
+
+// The arguments that the attention calls share, into the launch description.
+int check_attend(AttendLaunch& a, const uint16_t* Q, const uint16_t* k_pages,
+                 const uint16_t* v_pages, const int32_t* block_tables, int max_blocks, int page_size,
+                 int64_t n_pages, int n_seq, int n_tok, int H, int H_kv, int d, float scale,
+                 uint16_t* out, float* lse) {
+  if (!Q || !aligned16(Q) || !k_pages || !aligned16(k_pages) || !v_pages || !aligned16(v_pages) ||
+      !block_tables || !aligned4(block_tables) || !out || !aligned16(out) || !aligned4(lse) ||
+      n_seq < 0 || n_tok < 0 || max_blocks < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 ||
+      !(scale > 0.0f) || !std::isfinite(scale))
+    return MISA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || (d != 64 && d != 128) || H / H_kv > 128) return MISA_ERR_UNSUPPORTED;
+  if (n_pages < 1 || n_pages > (0x7fffffffLL >> shift)) return MISA_ERR_INVALID_ARG;
+  a.Q = Q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.block_tables = block_tables;
+  a.max_blocks = max_blocks;
+  a.page_shift = shift;
+  a.n_pages = n_pages;
+  a.n_seq = n_seq;
+  a.n_tok = n_tok;
+  a.H = H;
+  a.Hkv = H_kv;
+  a.d = d;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
   return MISA_OK;
 }
 
@@ -660,6 +736,216 @@ int misa_decode_score_topk(const uint16_t* Q, const float* w, const int32_t* hea
   return cuda_status(launch_topk(logits, ld, n_seq, 0, max_len, k, idx, ctl, s, nullptr, seq_lens));
 }
 
+int misa_plan_step(const int32_t* q_lens, const int32_t* ctx_lens, int n_seq, int32_t* block_tables,
+                   int max_blocks, int page_size, int64_t n_pages, int n_tok,
+                   const int32_t* free_pages, int64_t free_cap, const int32_t* free_count,
+                   int32_t* cu_q, int32_t* seq_lens, int32_t* positions, int32_t* slots,
+                   int32_t* seq_of, int32_t* granted, int32_t* free_count_out, void* stream) {
+  if (n_seq < 0 || n_tok < 0 || max_blocks < 1) return MISA_ERR_INVALID_ARG;
+  for (const void* q : {static_cast<const void*>(q_lens), static_cast<const void*>(ctx_lens),
+                        static_cast<const void*>(block_tables), static_cast<const void*>(cu_q),
+                        static_cast<const void*>(seq_lens), static_cast<const void*>(granted)})
+    if (!q || !aligned4(q)) return MISA_ERR_INVALID_ARG;
+  for (const void* q : {static_cast<const void*>(positions), static_cast<const void*>(slots),
+                        static_cast<const void*>(seq_of)})
+    if (n_tok > 0 && (!q || !aligned4(q))) return MISA_ERR_INVALID_ARG;
+  if (free_pages && (!aligned4(free_pages) || free_cap < 0 || free_cap > 0x7fffffffLL ||
+                     !free_count || !aligned4(free_count) || !free_count_out ||
+                     !aligned4(free_count_out)))
+    return MISA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || n_seq > plan_max_seq()) return MISA_ERR_UNSUPPORTED;
+  if (n_pages < 1 || n_pages > (0x7fffffffLL >> shift)) return MISA_ERR_INVALID_ARG;
+  DevCtl ctl;
+  if (!make_ctl(ctl)) return MISA_ERR_CUDA;
+  return cuda_status(launch_plan(q_lens, ctx_lens, n_seq, block_tables, max_blocks, shift, n_pages,
+                                 n_tok, free_pages, free_cap, free_count, cu_q, seq_lens, positions,
+                                 slots, seq_of, granted, free_count_out, ctl, as_stream(stream)));
+}
+
+int misa_release_pages(const int32_t* release, int32_t* seq_lens, const int32_t* block_tables,
+                       int n_seq, int max_blocks, int page_size, int64_t n_pages,
+                       int32_t* free_pages, int64_t free_cap, int32_t* free_count, void* stream) {
+  if (n_seq < 0 || max_blocks < 1 || free_cap < 0 || free_cap > 0x7fffffffLL)
+    return MISA_ERR_INVALID_ARG;
+  for (const void* q : {static_cast<const void*>(release), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(block_tables), static_cast<const void*>(free_pages),
+                        static_cast<const void*>(free_count)})
+    if (!q || !aligned4(q)) return MISA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0 || n_seq > plan_max_seq()) return MISA_ERR_UNSUPPORTED;
+  if (n_pages < 1 || n_pages > (0x7fffffffLL >> shift)) return MISA_ERR_INVALID_ARG;
+  if (n_seq == 0) return MISA_OK;
+  DevCtl ctl;
+  if (!make_ctl(ctl)) return MISA_ERR_CUDA;
+  return cuda_status(launch_release(release, seq_lens, block_tables, n_seq, max_blocks, shift,
+                                    n_pages, free_pages, free_cap, free_count, ctl,
+                                    as_stream(stream)));
+}
+
+int misa_rope_frequencies(int rope_dim, double base, int scaling, double factor, double trained_len,
+                          double fast_turns, double slow_turns, double* inv_freq,
+                          double* amplitude) {
+  if (rope_dim < 2 || rope_dim % 2 != 0 || rope_dim > 1024 || !(base > 1.0) || !inv_freq ||
+      !amplitude || !std::isfinite(base))
+    return MISA_ERR_INVALID_ARG;
+  if (scaling < MISA_ROPE_PLAIN || scaling > MISA_ROPE_BANDS) return MISA_ERR_INVALID_ARG;
+  if (scaling != MISA_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return MISA_ERR_INVALID_ARG;
+  if (scaling == MISA_ROPE_BANDS && (!(trained_len > 0.0) || !(slow_turns > 0.0) ||
+                                     !(fast_turns > slow_turns) || !std::isfinite(trained_len) ||
+                                     !std::isfinite(fast_turns)))
+    return MISA_ERR_INVALID_ARG;
+  if (scaling == MISA_ROPE_BASE && rope_dim == 2) return MISA_ERR_INVALID_ARG;
+  rope_frequencies(rope_dim, base, scaling, factor, trained_len, fast_turns, slow_turns, inv_freq,
+                   amplitude);
+  return MISA_OK;
+}
+
+int misa_rope(const uint16_t* X, const int32_t* positions, const double* inv_freq, int n, int H,
+              int d, int rope_dim, int offset, int interleaved, float amplitude, int transpose,
+              uint16_t* Y, void* stream) {
+  if (const int st = check_rope(X, positions, inv_freq, n, H, d, rope_dim, offset, interleaved,
+                                amplitude))
+    return st;
+  if (!Y || !aligned16(Y) || (transpose != 0 && transpose != 1)) return MISA_ERR_INVALID_ARG;
+  if (n == 0) return MISA_OK;
+  DevCtl ctl;
+  if (!make_ctl(ctl)) return MISA_ERR_CUDA;
+  RopeLaunch a{};
+  a.x = X;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.y = Y;
+  a.n = n;
+  a.H = H;
+  a.d = d;
+  a.rope_dim = rope_dim;
+  a.offset = offset;
+  a.interleaved = interleaved != 0;
+  a.transpose = transpose != 0;
+  a.amplitude = amplitude;
+  return cuda_status(launch_rope(a, ctl, as_stream(stream)));
+}
+
+int misa_rope_fp8(const uint16_t* X, const int32_t* positions, const double* inv_freq, int n, int H,
+                  int d, int rope_dim, int offset, int interleaved, float amplitude, uint8_t* Y8,
+                  float* y_scale, void* stream) {
+  if (const int st = check_rope(X, positions, inv_freq, n, H, d, rope_dim, offset, interleaved,
+                                amplitude))
+    return st;
+  if (!Y8 || !aligned16(Y8) || !y_scale || !aligned4(y_scale)) return MISA_ERR_INVALID_ARG;
+  if (n == 0) return MISA_OK;
+  DevCtl ctl;
+  if (!make_ctl(ctl)) return MISA_ERR_CUDA;
+  RopeLaunch a{};
+  a.x = X;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.y8 = Y8;
+  a.scale = y_scale;
+  a.n = n;
+  a.H = H;
+  a.d = d;
+  a.rope_dim = rope_dim;
+  a.offset = offset;
+  a.interleaved = interleaved != 0;
+  a.amplitude = amplitude;
+  return cuda_status(launch_rope(a, ctl, as_stream(stream)));
+}
+
+int misa_cache_append(const uint16_t* K, const uint16_t* V, const int32_t* positions,
+                      const int32_t* slots, const double* inv_freq, int n, int H, int d,
+                      int rope_dim, int offset, int interleaved, float amplitude, int kdtype,
+                      void* k_pages, float* k_scale, uint16_t* v_pages, int page_size,
+                      int64_t n_pages, void* stream) {
+  if (const int st = check_rope(K, positions, inv_freq, n, H, d, rope_dim, offset, interleaved,
+                                amplitude))
+    return st;
+  if (!slots || !aligned4(slots) || !k_pages || !aligned16(k_pages) || !V != !v_pages ||
+      (V && (!aligned16(V) || !aligned16(v_pages))))
+    return MISA_ERR_INVALID_ARG;
+  if (kdtype != MISA_K_BF16 && kdtype != MISA_K_FP8E4M3) return MISA_ERR_INVALID_ARG;
+  if (kdtype == MISA_K_FP8E4M3 && (!k_scale || !aligned4(k_scale))) return MISA_ERR_INVALID_ARG;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0) return MISA_ERR_UNSUPPORTED;
+  if (n_pages < 1 || n_pages > (0x7fffffffLL >> shift)) return MISA_ERR_INVALID_ARG;
+  if (n == 0) return MISA_OK;
+  DevCtl ctl;
+  if (!make_ctl(ctl)) return MISA_ERR_CUDA;
+  RopeLaunch a{};
+  a.x = K;
+  a.v = V;
+  a.positions = positions;
+  a.slots = slots;
+  a.inv_freq = inv_freq;
+  if (kdtype == MISA_K_FP8E4M3) {
+    a.y8 = static_cast<uint8_t*>(k_pages);
+    a.scale = k_scale;
+  } else {
+    a.y = static_cast<uint16_t*>(k_pages);
+  }
+  a.v_pages = v_pages;
+  a.rows_cap = n_pages << shift;
+  a.n = n;
+  a.H = H;
+  a.d = d;
+  a.rope_dim = rope_dim;
+  a.offset = offset;
+  a.interleaved = interleaved != 0;
+  a.amplitude = amplitude;
+  return cuda_status(launch_rope(a, ctl, as_stream(stream)));
+}
+
+int misa_attend_paged(const uint16_t* Q, const uint16_t* k_pages, const uint16_t* v_pages,
+                      const int32_t* block_tables, int max_blocks, int page_size, int64_t n_pages,
+                      const int32_t* cu_q, const int32_t* seq_lens, int n_seq, int n_tok, int H,
+                      int H_kv, int d, float scale, int window, int sinks, uint16_t* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream) {
+  if (!cu_q || !aligned4(cu_q) || !seq_lens || !aligned4(seq_lens) || window < 0 || sinks < 0 ||
+      (window == 0 && sinks > 0))
+    return MISA_ERR_INVALID_ARG;
+  AttendLaunch a{};
+  if (const int st = check_attend(a, Q, k_pages, v_pages, block_tables, max_blocks, page_size,
+                                  n_pages, n_seq, n_tok, H, H_kv, d, scale, out, lse))
+    return st;
+  if (n_tok == 0 || n_seq == 0) return MISA_OK;
+  if (!ws || !aligned16(ws) || ws_bytes < attend_workspace(d)) return MISA_ERR_WORKSPACE;
+  DevCtl ctl;
+  if (!make_ctl(ctl)) return MISA_ERR_CUDA;
+  a.cu_q = cu_q;
+  a.seq_lens = seq_lens;
+  a.window = window;
+  a.sinks = sinks;
+  a.ws = ws;
+  return cuda_status(launch_attend(a, ctl, as_stream(stream)));
+}
+
+int misa_attend_selected(const uint16_t* Q, const uint16_t* k_pages, const uint16_t* v_pages,
+                         const int32_t* block_tables, int max_blocks, int page_size,
+                         int64_t n_pages, const int32_t* seq_of, const int32_t* positions,
+                         const int32_t* idx, int k, int n_seq, int n_tok, int H, int H_kv, int d,
+                         float scale, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                         void* stream) {
+  if (!seq_of || !aligned4(seq_of) || !positions || !aligned4(positions) || !idx || !aligned4(idx) ||
+      k < 1 || k > 16384)
+    return MISA_ERR_INVALID_ARG;
+  AttendLaunch a{};
+  if (const int st = check_attend(a, Q, k_pages, v_pages, block_tables, max_blocks, page_size,
+                                  n_pages, n_seq, n_tok, H, H_kv, d, scale, out, lse))
+    return st;
+  if (n_tok == 0 || n_seq == 0) return MISA_OK;
+  if (!ws || !aligned16(ws) || ws_bytes < attend_workspace(d)) return MISA_ERR_WORKSPACE;
+  DevCtl ctl;
+  if (!make_ctl(ctl)) return MISA_ERR_CUDA;
+  a.seq_of = seq_of;
+  a.positions = positions;
+  a.idx = idx;
+  a.k = k;
+  a.ws = ws;
+  return cuda_status(launch_attend(a, ctl, as_stream(stream)));
+}
+
 int misa_profile_start(void) {
   std::lock_guard<std::mutex> lk(g_prof.mu);
   for (int i = 0; i < kStages; ++i) {
@@ -711,6 +997,7 @@ size_t misa_workspace_size(const char* op, int n_q, int64_t n_k, int k, int kp) 
     if (k <= 0 || k > kFusedMaxK || n_k > kFusedMaxKeys || n_k < kSampleKeys) return 0;
     return FusedLayout(n_q, n_k).total;
   }
+  if (std::strcmp(op, "attend") == 0) return k == 64 || k == 128 ? attend_workspace(k) : 0;
   return 0;
 }
 

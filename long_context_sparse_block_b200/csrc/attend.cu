@@ -1,0 +1,1226 @@
+// Attention of new tokens over paged key and value caches: over everything a
+// query sees (optionally a sliding window and a few first tokens), or over the
+// query's own list of tokens.
+//
+//   o_t,h = sum_s exp(z_s - lse) v_s,  z_s = scale * q_t,h . k_s,
+//   lse = log sum_s exp(z_s),  s over the keys that query t sees.
+//
+// One pass over the keys with a running reference m and sum l of each row: a
+// tile of 128 keys gives S = Q K^T on the tensor cores (fp32 in TMEM), the rows'
+// threads turn it into P = 2^(c S - m) (c = scale log2 e; bf16, written back to
+// TMEM over S) and O += P V follows on the tensor cores (P from TMEM, V from
+// shared memory as an MN-major operand, O fp32 in TMEM).  m is only raised when
+// a row's maximum passes it by more than 8 (so P <= 2^8, exact in bf16's range,
+// and l stays far inside fp32's): O is then rescaled in TMEM, which is rare.
+// l sums the unrounded fp32 weights; the rounding of P to bf16 is the one that
+// the tensor cores ask for (relative 2^-8 per weight, averaged over the sum).
+//
+// Rows.  The G = H / Hkv query heads that share a key head are rows of one
+// matrix: row r of (sequence, key head) is query r / G, head r % G, so every key
+// tile serves 128 rows even for few tokens.  A unit is (sequence, block of 256
+// rows, key head); its two slots are two 128-row halves, each with its own
+// softmax warpgroup, S / P and O: while one slot's rows are exponentiated the
+// tensor cores work for the other.  A unit of at most 128 rows (decode, ragged
+// ends, the list form) uses the two slots for the same rows and alternate tiles
+// instead, which keeps the same overlap, and joins the two O in TMEM at the end.
+//
+// Split.  The units' cost (a closed form, linear in the row block) is laid on a
+// line that is cut evenly over the CTAs; a unit cut by a boundary leaves
+// unnormalised O, m and l of each part in the workspace (at most two parts per
+// CTA) and a second kernel joins them in a fixed order.  So one new token over a
+// long cache fills the chip as well as a long chunk does, lengths stay on the
+// device, and results do not depend on timing.
+//
+// Warps: 0 key / value loader (TMA boxes, one per page, through the block
+// table; the list form loads rows by cp.async from four warps of its own),
+// 1 MMA issuer, 3 scheduler, 2 query loader (and the zeroing of value rows past the end of
+// a sequence, which may hold anything, before the MMA reads them: 0 * NaN is
+// NaN), 4-7 and 8-11 the softmax of slots 0 and 1.
+#include <cstring>
+
+#include "internal.h"
+
+namespace misa {
+namespace {
+
+constexpr int kTile = 128;       // keys per tile
+constexpr int kBlockRows = 256;  // rows of a unit (two slots of 128)
+constexpr int kSegs = 4;         // segments published ahead
+constexpr uint64_t kDrainNs = 2000000;
+constexpr float kRaise = 8.0f;   // log2 of the largest weight before m is raised
+
+template <int D, bool LIST>
+struct AttLayout {
+  static constexpr int THREADS = LIST ? 512 : 384;
+  static constexpr int CH = D / 64;              // 128-byte wide chunks of a row
+  static constexpr int CHUNK = kTile * 128;      // bytes of one chunk of a tile
+  static constexpr int TILE = CH * CHUNK;        // a key or value tile
+  static constexpr int QTILE = kTile * D * 2;    // 128 query rows, same layout
+  static constexpr int STAGES = (LIST ? 6 : 5) * (D == 128 ? 1 : 2);
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_KV = OFF_Q + (LIST ? 1 : 2) * QTILE;
+  static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
+  static constexpr int NBAR = 2 * STAGES + 14 + 2 * kSegs;
+  static constexpr int OFF_SEG = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;
+  static constexpr int OFF_ML = OFF_SEG + kSegs * 64;  // slot 1's (m, l) of 128 rows
+  static constexpr int OFF_MISC = OFF_ML + 128 * 8;
+  static constexpr int BYTES = OFF_MISC + 16;
+  // warps that read a segment: loader (list form: its four), MMA, queries, softmax
+  static constexpr int SEG_READERS = (LIST ? 4 : 1) + 1 + 1 + 8;
+  static constexpr int ALLOC = BYTES + 1024;
+  static_assert(ALLOC <= 232448, "shared memory of an SM");
+};
+
+struct AttParams {
+  const uint16_t* Q;        // [n_tok, H, D]
+  const uint16_t* kp;       // [n_pages, page, Hkv, D]
+  const uint16_t* vp;
+  const int32_t* bts;       // [n_seq, max_blocks]
+  const int32_t* cu_q;      // [n_seq + 1]
+  const int32_t* lens;      // [n_seq]
+  const int32_t* seq_of;    // list form: [n_tok]
+  const int32_t* positions; // list form: [n_tok]
+  const int32_t* idx;       // list form: [n_tok, k]
+  uint16_t* out;            // [n_tok, H, D]
+  float* lse;               // [n_tok, H], nullable
+  int64_t n_pages;
+  int64_t key_rows;
+  int max_blocks;
+  int page_shift;
+  int n_seq;
+  int n_tok;
+  int H;
+  int Hkv;
+  int G;
+  int window;               // 0: none
+  int sinks;
+  int k;
+  float c;                  // scale * log2(e)
+  // workspace
+  int4* head;               // [ctas][2]: what each CTA left in parts
+  float* ml;                // [2 ctas][256][2]
+  float* po;                // [2 ctas][256][D]
+  DevCtl ctl;
+};
+
+// ---- units -------------------------------------------------------------------
+
+struct Unit {
+  int b;       // sequence (list form: unused)
+  int m;       // row block (list form: token)
+  int j;       // key head
+  int64_t off; // cost already spent of this unit
+};
+
+struct SeqInfo {
+  int64_t t0;  // first row of the packed batch
+  int n;       // new tokens
+  int len;     // keys
+  int p0;      // position of the first new token
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttParams& p, int b) {
+  SeqInfo s;
+  int t0 = __ldg(p.cu_q + b), t1 = __ldg(p.cu_q + b + 1);
+  t0 = min(max(t0, 0), p.n_tok);
+  t1 = min(max(t1, t0), p.n_tok);
+  int64_t len = __ldg(p.lens + b);
+  const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
+  len = len < 0 ? 0 : len > cap ? cap : len;
+  s.t0 = t0;
+  s.n = t1 - t0;
+  s.len = static_cast<int>(len);
+  s.p0 = s.len - s.n;
+  return s;
+}
+
+__device__ __forceinline__ int64_t row_blocks(const AttParams& p, const SeqInfo& s) {
+  return (static_cast<int64_t>(s.n) * p.G + kBlockRows - 1) / kBlockRows;
+}
+
+// Cost of row block m of a sequence and its sum over blocks 0..m-1: about the
+// keys it passes over, times G.  Only the balance depends on it.
+__device__ __forceinline__ int64_t cost_flat(const AttParams& p) {
+  return p.window ? static_cast<int64_t>(p.G) * (static_cast<int64_t>(p.window) + p.sinks + 2 * kTile) +
+                        kBlockRows
+                  : 0x3fffffffffffffffLL;
+}
+__device__ __forceinline__ int64_t cost_of(const AttParams& p, const SeqInfo& s, int64_t m) {
+  const int64_t c = static_cast<int64_t>(p.G) * (max(s.p0, 0) + kTile) + kBlockRows * (m + 1);
+  return min(c, cost_flat(p));
+}
+__device__ __forceinline__ int64_t cost_before(const AttParams& p, const SeqInfo& s, int64_t m) {
+  const int64_t base = static_cast<int64_t>(p.G) * (max(s.p0, 0) + kTile);
+  const int64_t flat = cost_flat(p);
+  // blocks below `lin` grow with m, those from it on cost `flat`
+  int64_t lin = flat > base ? (flat - base) / kBlockRows : 0;
+  lin = min(lin, m);
+  return lin * base + kBlockRows * (lin * (lin + 1) / 2) + (m - lin) * (m > lin ? flat : 0);
+}
+
+// Tiles of a unit: `sink` tiles from the start, then tiles lo.. .
+struct Tiles {
+  int n;     // tiles in all
+  int sink;
+  int lo;
+  int rows;  // valid rows of the unit
+};
+
+__device__ __forceinline__ Tiles unit_tiles(const AttParams& p, const SeqInfo& s, int m) {
+  Tiles t;
+  const int64_t r0 = static_cast<int64_t>(m) * kBlockRows;
+  const int64_t all = static_cast<int64_t>(s.n) * p.G;
+  t.rows = static_cast<int>(min(static_cast<int64_t>(kBlockRows), all - r0));
+  const int p_first = s.p0 + static_cast<int>(r0 / p.G);
+  const int p_last = s.p0 + static_cast<int>((r0 + t.rows - 1) / p.G);
+  const int end = p_last < 0 ? 1 : p_last / kTile + 1;  // a unit that sees nothing passes one tile
+  t.lo = 0;
+  t.sink = 0;
+  if (p.window) {
+    const int64_t f = static_cast<int64_t>(p_first) - p.window + 1;
+    t.lo = f > 0 ? static_cast<int>(f / kTile) : 0;
+    t.sink = min((p.sinks + kTile - 1) / kTile, t.lo);
+  }
+  t.n = t.sink + end - t.lo;
+  return t;
+}
+
+// What the roles work on: tiles [i0, i1) of a unit, whole or a part.  Written to
+// shared memory by the scheduling warp, a few ahead.
+struct __align__(16) Seg {
+  int valid;   // 0: the end
+  int t0;      // first row of the sequence in the packed batch (list form: the token)
+  int len;     // keys of the sequence
+  int p0;      // position of the first new token (list form: of the token)
+  int b, m, j;
+  int i0, i1;
+  int part;    // workspace slot, or -1: the whole unit
+  int split;   // both slots share the rows (alternate tiles)
+  int rows;    // valid rows of the unit
+  int sink, lo;
+  int pad[2];
+  __device__ __forceinline__ int key0(int i) const { return (i < sink ? i : lo + i - sink) * kTile; }
+  // tiles of a slot
+  __device__ __forceinline__ int tiles_of(int slot) const {
+    const int n = i1 - i0;
+    return split ? (n + 1 - slot) >> 1 : n;
+  }
+};
+static_assert(sizeof(Seg) == 64, "segment slot");
+
+// Where the CTA's stretch of the line begins and how long it is.
+struct Start {
+  Unit u;
+  int64_t left;
+};
+
+template <bool LIST>
+struct Walk {
+  Unit u;
+  int64_t left;
+  int cta;
+  __device__ __forceinline__ void init(const Start& st, int c) {
+    u = st.u;
+    left = st.left;
+    cta = c;
+  }
+  // The next non-empty segment; valid = 0 at the end of the stretch.
+  __device__ __forceinline__ void next(const AttParams& p, Seg& g) {
+    g.valid = 0;
+    while (left > 0) {
+      if constexpr (LIST) {
+        if (u.m >= p.n_tok) return;
+        const int nt = (p.k + kTile - 1) / kTile;
+        g.i0 = static_cast<int>(u.off);
+        g.i1 = static_cast<int>(min(static_cast<int64_t>(nt), u.off + left));
+        g.b = __ldg(p.seq_of + u.m);
+        g.m = u.m;
+        g.j = u.j;
+        left -= g.i1 - g.i0;
+        u.off = 0;
+        if (++u.j == p.Hkv) {
+          u.j = 0;
+          ++u.m;
+        }
+        if (g.b < 0) continue;  // a row of no sequence: left as it was
+        if (g.b >= p.n_seq) {
+          report(p.ctl, DEV_BAD_INPUT);
+          continue;
+        }
+        g.t0 = g.m;
+        g.p0 = __ldg(p.positions + g.m);
+        g.len = 0;
+        g.rows = p.G;
+        g.sink = g.lo = 0;
+        g.split = 1;
+        g.part = g.i0 > 0 ? 2 * cta : g.i1 < nt ? 2 * cta + 1 : -1;
+        g.valid = 1;
+        return;
+      } else {
+        if (u.b >= p.n_seq) return;
+        const SeqInfo s = seq_info(p, u.b);
+        if (s.n == 0) {
+          ++u.b;
+          continue;
+        }
+        const Tiles t = unit_tiles(p, s, u.m);
+        const int64_t cost = cost_of(p, s, u.m);
+        const int64_t end = min(cost, u.off + left);
+        g.i0 = static_cast<int>(u.off * t.n / cost);
+        g.i1 = static_cast<int>(end * t.n / cost);
+        g.b = u.b;
+        g.m = u.m;
+        g.j = u.j;
+        left -= end - u.off;
+        u.off = 0;
+        if (++u.j == p.Hkv) {
+          u.j = 0;
+          if (++u.m >= row_blocks(p, s)) {
+            u.m = 0;
+            ++u.b;
+          }
+        }
+        if (g.i1 <= g.i0) continue;
+        g.t0 = static_cast<int>(s.t0);
+        g.len = s.len;
+        g.p0 = s.p0;
+        g.rows = t.rows;
+        g.sink = t.sink;
+        g.lo = t.lo;
+        g.split = t.rows <= kTile;
+        g.part = g.i0 > 0 ? 2 * cta : g.i1 < t.n ? 2 * cta + 1 : -1;
+        g.valid = 1;
+        return;
+      }
+    }
+  }
+};
+
+// All threads: finds the unit at point x of the line (x in [0, total)).  Called
+// with the block's prefix of sequence costs in hand.
+__device__ __forceinline__ void locate(const AttParams& p, int b, int64_t x, Unit& u) {
+  const SeqInfo s = seq_info(p, b);
+  int64_t lo = 0, hi = row_blocks(p, s) - 1;
+  while (lo < hi) {  // the last block that starts at or before x
+    const int64_t mid = (lo + hi + 1) >> 1;
+    if (cost_before(p, s, mid) * p.Hkv <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  x -= cost_before(p, s, lo) * p.Hkv;
+  const int64_t c = cost_of(p, s, lo);
+  u.b = b;
+  u.m = static_cast<int>(lo);
+  u.j = static_cast<int>(x / c);
+  u.off = x % c;
+}
+
+struct PlanShared {
+  Unit at[2];       // the units at the two ends of the stretch
+  int64_t ends[2];
+  int64_t warp_sum[16];
+  int64_t carry;
+};
+
+// Scans the sequences' costs and finds this CTA's stretch [total c / n, total
+// (c + 1) / n).  Two passes over the sequences when the threads do not hold them
+// all (their lengths are in cache by then).
+template <int THREADS>
+__device__ __forceinline__ void plan_stretch(const AttParams& p, PlanShared& ps, Start& st) {
+  const int tid = threadIdx.x;
+  int64_t total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t carry = 0;
+    int64_t x0 = 0, x1 = 0;
+    if (pass == 1) {
+      const int64_t n = gridDim.x, c = blockIdx.x;
+      x0 = total / n * c + total % n * c / n;
+      x1 = total / n * (c + 1) + total % n * (c + 1) / n;
+      if (tid == 0) {
+        ps.ends[0] = x0;
+        ps.ends[1] = x1;
+        ps.at[0] = Unit{p.n_seq, 0, 0, 0};
+        ps.at[1] = Unit{p.n_seq, 0, 0, 0};
+      }
+    }
+    for (int base = 0; base < p.n_seq; base += THREADS) {
+      const int b = base + tid;
+      int64_t cost = 0;
+      if (b < p.n_seq) {
+        const SeqInfo s = seq_info(p, b);
+        if (pass == 0) {
+          const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
+          const int len = __ldg(p.lens + b);
+          if (len < 0 || len > cap) report(p.ctl, DEV_BAD_INPUT);
+        }
+        if (s.n > 0) cost = cost_before(p, s, row_blocks(p, s)) * p.Hkv;
+      }
+      int64_t x = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane_id() >= o) x += y;
+      }
+      __syncthreads();
+      if (lane_id() == 31) ps.warp_sum[warp_id()] = x;
+      __syncthreads();
+      int64_t before = carry;
+      for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp_id()) before += ps.warp_sum[w];
+        carry += ps.warp_sum[w];
+      }
+      if (pass == 1 && cost > 0) {
+        const int64_t lo = before + x - cost, hi = before + x;
+        if (x0 >= lo && x0 < hi) locate(p, b, x0 - lo, ps.at[0]);
+        if (x1 >= lo && x1 < hi) locate(p, b, x1 - lo, ps.at[1]);
+      }
+    }
+    total = carry;
+    __syncthreads();
+  }
+  st.u = ps.at[0];
+  st.left = ps.ends[1] - ps.ends[0];
+}
+
+// Tile boundary of a unit at cost offset `off`.
+__device__ __forceinline__ int tile_at(const AttParams& p, const Unit& u, int& n) {
+  const SeqInfo s = seq_info(p, u.b);
+  const Tiles t = unit_tiles(p, s, u.m);
+  n = t.n;
+  return static_cast<int>(u.off * t.n / cost_of(p, s, u.m));
+}
+
+// What the CTA will leave in the workspace, for the joining kernel:
+//   head[2 c]     x: 1 if it continues a unit that an earlier CTA opened with at
+//                 least one tile, y: 1 if the unit ends here
+//   head[2 c + 1] x: 1 if it opens a unit that it does not finish, y: sequence
+//                 (list form: 0), z: row block (token), w: key head
+template <bool LIST>
+__device__ __forceinline__ void write_head(const AttParams& p, const Start& st, const Unit& end) {
+  const int c = blockIdx.x;
+  int4 cont = make_int4(0, 0, 0, 0), open = make_int4(0, 0, 0, 0);
+  const int past = LIST ? p.n_tok : p.n_seq;
+  const int key_s = LIST ? st.u.m : st.u.b, key_e = LIST ? end.m : end.b;
+  const bool same = st.u.b == end.b && st.u.m == end.m && st.u.j == end.j;
+  int i0 = 0, i1 = 0, n = 0;
+  if (key_s < past) {
+    if (LIST) {
+      n = (p.k + kTile - 1) / kTile;
+      i0 = static_cast<int>(st.u.off);
+    } else {
+      i0 = tile_at(p, st.u, n);
+    }
+    if (i0 > 0) {
+      int n2;
+      i1 = !same ? n : LIST ? static_cast<int>(end.off) : tile_at(p, end, n2);
+      cont.x = i1 > i0;
+      cont.y = i1 >= n;
+    }
+  }
+  if (key_e < past && end.off > 0 && !(same && i0 > 0) && st.left > 0) {
+    int n2 = (p.k + kTile - 1) / kTile;
+    const int e = LIST ? static_cast<int>(end.off) : tile_at(p, end, n2);
+    if (e > 0 && e < n2) open = make_int4(1, LIST ? 0 : end.b, end.m, end.j);
+    // (e == n2: whole; the row of no sequence of the list form is skipped by all)
+  }
+  p.head[2 * c] = cont;
+  p.head[2 * c + 1] = open;
+}
+
+// ---- small device helpers --------------------------------------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// The low n bits (n clamped to 0..32).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate.
+__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// MN-major operand in 128-byte swizzled rows: 64 elements of N per row, one row
+// per k; 8-row atoms of 1024 bytes along k (stride field), chunks of 64 along N
+// `chunk` bytes apart (leading field).
+__device__ __forceinline__ uint64_t umma_desc_mnmajor(uint32_t saddr, uint32_t chunk) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(chunk >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= 1ull << 46;
+  d |= 2ull << 61;
+  return d;
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Every lane waits; true when all got through.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          const DevCtl& ctl) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, ctl));
+}
+
+// Places of a segment's tiles in the ring: K_0, K_1, V_0, K_2, V_1, .., V_{n-1}.
+__device__ __forceinline__ uint32_t k_at(int x) { return x == 0 ? 0u : 2u * x - 1u; }
+__device__ __forceinline__ uint32_t v_at(int x, int n) { return x == n - 1 ? 2u * n - 1u : 2u * x + 2u; }
+
+// Unnormalised O of a TMEM row, 32 columns at a time, to f(column, values).
+template <int D, typename F>
+__device__ __forceinline__ void for_o(uint32_t taddr, F&& f) {
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t v[32];
+    tmem_ld32(taddr + c0, v);
+    tmem_wait_ld_regs(v);
+    f(c0, v);
+  }
+}
+
+template <int D, bool LIST>
+__global__ void __launch_bounds__(AttLayout<D, LIST>::THREADS, 1)
+attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+              const AttParams p) {
+  using L = AttLayout<D, LIST>;
+  constexpr int ST = L::STAGES;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1024(smem_raw);
+  PlanShared& ps = *reinterpret_cast<PlanShared*>(smem);  // before the query rows arrive
+  const uint32_t sQ = smem_u32(smem + L::OFF_Q);
+  const uint32_t sKV = smem_u32(smem + L::OFF_KV);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  constexpr int FULL = 0, EMPTY = ST, QFULL = 2 * ST, QEMPTY = QFULL + 1, SFULL = QFULL + 2,
+                PFULL = SFULL + 2, OFULL = PFULL + 2, OEMPTY = OFULL + 2, MLFULL = OEMPTY + 2,
+                MLEMPTY = MLFULL + 1, VREADY = MLEMPTY + 1, VTAIL = VREADY + 1, GFULL = VTAIL + 1,
+                GEMPTY = GFULL + kSegs;
+  static_assert(GEMPTY + kSegs == L::NBAR, "barriers");
+  Seg* segs = reinterpret_cast<Seg*>(smem + L::OFF_SEG);
+  float2* ml1 = reinterpret_cast<float2*>(smem + L::OFF_ML);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
+  const int warp = warp_id(), lane = lane_id();
+
+  Start st;
+  if constexpr (LIST) {
+    // every unit costs its tiles: the stretch is a division away
+    const int64_t nt = (p.k + kTile - 1) / kTile;
+    const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * nt;
+    const int64_t n = gridDim.x, c = blockIdx.x;
+    const int64_t x0 = total / n * c + total % n * c / n;
+    const int64_t x1 = total / n * (c + 1) + total % n * (c + 1) / n;
+    auto unit = [&](int64_t x) {
+      const int64_t q = x / nt;
+      return Unit{0, static_cast<int>(q / p.Hkv), static_cast<int>(q % p.Hkv), x % nt};
+    };
+    st.u = unit(x0);
+    st.left = x1 - x0;
+    if (threadIdx.x == 0) write_head<true>(p, st, unit(x1));
+  } else {
+    plan_stretch<L::THREADS>(p, ps, st);
+    if (threadIdx.x == 0) write_head<false>(p, st, ps.at[1]);
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(bar(FULL + i), LIST ? 128 : 1);
+      mbar_init(bar(EMPTY + i), 1);
+    }
+    mbar_init(bar(QFULL), 32);
+    mbar_init(bar(QEMPTY), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(SFULL + i), 1);
+      mbar_init(bar(PFULL + i), 4);
+      mbar_init(bar(OFULL + i), 1);
+      mbar_init(bar(OEMPTY + i), 4);
+    }
+    mbar_init(bar(MLFULL), 4);
+    mbar_init(bar(MLEMPTY), 4);
+    mbar_init(bar(VREADY), 1);
+    mbar_init(bar(VTAIL), 1);
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(bar(GFULL + i), 1);
+      mbar_init(bar(GEMPTY + i), L::SEG_READERS);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    if (!LIST) {
+      tma_prefetch_desc(&kmap);
+      tma_prefetch_desc(&vmap);
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  // Segment number e, read from shared memory by the lanes that wait for it;
+  // every reading warp gives its slot back once.
+  auto seg_at = [&](uint32_t e) -> const Seg& { return segs[e % kSegs]; };
+  auto seg_wait = [&](uint32_t e) -> bool {
+    return mbar_wait(bar(GFULL + e % kSegs), (e / kSegs) & 1, abort_flag, p.ctl) && seg_at(e).valid;
+  };
+  auto seg_done = [&](uint32_t e) { mbar_arrive(bar(GEMPTY + e % kSegs)); };
+  uint32_t sg = 0;  // this role's segment number
+
+  if (warp < 4) {
+    if constexpr (LIST) reg_dec<64>(); else reg_dec<72>();
+  if (warp == 0) {
+    if constexpr (!LIST) {
+      // -------------------------------------------------------- key / value loader
+      uint32_t ring = 0;
+      bool ok = true;
+      const int page = 1 << p.page_shift, per = kTile / page;
+      for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
+        const Seg g = seg_at(sg);
+        __syncwarp();
+        if (lane == 0) seg_done(sg);
+        const int n = g.i1 - g.i0;
+        const int32_t* bt = p.bts + static_cast<int64_t>(g.b) * p.max_blocks;
+        auto page_row = [&](int x) -> int {  // this lane's page of tile x
+          if (lane >= per || x >= n) return 0;
+          const int64_t s0 = static_cast<int64_t>(g.key0(g.i0 + x)) + lane * page;
+          int64_t y = p.key_rows;  // past the sequence: a box of fill rows
+          if (s0 < g.len) {
+            int64_t pg = __ldg(bt + (s0 >> p.page_shift));
+            if (pg < 0 || pg >= p.n_pages) {
+              report(p.ctl, DEV_BAD_INPUT);
+              pg = 0;
+            }
+            y = pg << p.page_shift;
+          }
+          return static_cast<int>(y);
+        };
+        auto load = [&](const CUtensorMap* map, uint32_t at, int y) -> bool {
+          const uint32_t e = ring + at, stage = e % ST, phase = (e / ST) & 1;
+          if (!warp_wait(bar(EMPTY + stage), phase ^ 1, abort_flag, p.ctl)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(bar(FULL + stage), L::TILE);
+          __syncwarp();
+          if (lane < per) {
+#pragma unroll
+            for (int c = 0; c < L::CH; ++c)
+              tma_load_3d(sKV + stage * L::TILE + c * L::CHUNK + lane * page * 128, map,
+                          bar(FULL + stage), c * 64, g.j, y);
+          }
+          return true;
+        };
+        int y_cur = page_row(0), y_next = page_row(1), y_prev = 0;
+        for (int x = 0; x <= n && ok; ++x) {
+          if (x < n) ok = load(&kmap, k_at(x), y_cur);
+          if (ok && x > 0) ok = load(&vmap, v_at(x - 1, n), y_prev);
+          y_prev = y_cur;
+          y_cur = y_next;
+          y_next = page_row(x + 2);
+        }
+        if (!ok) break;
+        ring += 2 * n;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      uint32_t ring = 0, tails = 0;
+      uint32_t used[2] = {0, 0};   // segments in which the slot had tiles
+      uint32_t pcount[2] = {0, 0}; // tiles of the slot so far
+      bool ok = true;
+      constexpr uint32_t id_qk = umma_idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t id_pv = umma_idesc_bf16_f32(kTile, D) | (1u << 16);  // B is MN-major
+      for (; seg_wait(sg); ++sg) {
+        const Seg g = seg_at(sg);
+        seg_done(sg);
+        const int n = g.i1 - g.i0;
+        const int n0 = g.tiles_of(0), n1 = g.tiles_of(1);
+        int qk_left = n0 + n1;
+        const bool tail = !LIST && g.len > g.key0(g.i1 - 1) && g.len < g.key0(g.i1 - 1) + kTile;
+        ok = mbar_wait(bar(QFULL), sg & 1, abort_flag, p.ctl);
+        if (!ok) break;
+        fence_proxy_async_smem();  // the query rows' copies -> MMA operand reads
+        bool told = !tail;
+        auto full = [&](uint32_t at, uint32_t& stage) -> bool {
+          const uint32_t e = ring + at;
+          stage = e % ST;
+          if (!mbar_wait(bar(FULL + stage), (e / ST) & 1, abort_flag, p.ctl)) return false;
+          // entries up to at - 2 have been waited for, so from here on the last
+          // tile's values are the next to fill their stage: its phase can be
+          // waited for by parity
+          if (!told && at + ST >= 2u * n + 1u) {
+            mbar_arrive(bar(VTAIL));
+            told = true;
+          }
+          if (LIST) fence_proxy_async_smem();
+          tc_fence_after();
+          return true;
+        };
+        auto qk = [&](int slot, int i) -> bool {  // S of the slot's i-th tile
+          const int x = g.split ? 2 * i + slot : i;
+          uint32_t stage;
+          if (!full(k_at(x), stage)) return false;
+          const uint32_t a = sQ + (g.split ? 0 : slot) * L::QTILE, b = sKV + stage * L::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t o = (kk / 4) * L::CHUNK + (kk % 4) * 32;
+            tc_mma_bf16(tmem_base + slot * kTile, umma_desc_kmajor(a + o, 128),
+                        umma_desc_kmajor(b + o, 128), id_qk, kk > 0 ? 1u : 0u);
+          }
+          if (g.split || slot == 1) tc_commit(bar(EMPTY + stage));
+          tc_commit(bar(SFULL + slot));
+          if (--qk_left == 0) tc_commit(bar(QEMPTY));  // the query rows are free again
+          return true;
+        };
+        auto pv = [&](int slot, int i) -> bool {  // O += P V of the slot's i-th tile
+          const int x = g.split ? 2 * i + slot : i;
+          uint32_t stage;
+          if (!full(v_at(x, n), stage)) return false;
+          if (tail && x == n - 1 && (g.split || slot == 0)) {
+            if (!mbar_wait(bar(VREADY), tails & 1, abort_flag, p.ctl)) return false;
+            fence_proxy_async_smem();
+          }
+          if (i == 0 &&
+              !mbar_wait(bar(OEMPTY + slot), (used[slot] & 1) ^ 1, abort_flag, p.ctl))
+            return false;
+          if (!mbar_wait(bar(PFULL + slot), pcount[slot] & 1, abort_flag, p.ctl)) return false;
+          tc_fence_after();
+          const uint32_t b = sKV + stage * L::TILE;
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_bf16_ta(tmem_base + 256 + slot * D, tmem_base + slot * kTile + kk * 8,
+                           umma_desc_mnmajor(b + kk * 2048, L::CHUNK), id_pv,
+                           i > 0 || kk > 0 ? 1u : 0u);
+          ++pcount[slot];
+          if (g.split || slot == 1) tc_commit(bar(EMPTY + stage));
+          if (i == g.tiles_of(slot) - 1) tc_commit(bar(OFULL + slot));
+          return true;
+        };
+        ok = qk(0, 0) && (n1 == 0 || qk(1, 0));
+        for (int i = 0; ok && i < n0; ++i) {
+          ok = pv(0, i) && (i + 1 >= n0 || qk(0, i + 1));
+          if (ok && i < n1) ok = pv(1, i) && (i + 1 >= n1 || qk(1, i + 1));
+        }
+        if (!ok) break;
+        ring += 2 * n;
+        ++used[0];
+        if (n1 > 0) ++used[1];
+        if (tail) ++tails;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ scheduler
+    if (lane == 0) {
+      Walk<LIST> walk;
+      walk.init(st, blockIdx.x);
+      for (;; ++sg) {
+        if (!mbar_wait(bar(GEMPTY + sg % kSegs), ((sg / kSegs) & 1) ^ 1, abort_flag, p.ctl)) break;
+        Seg g;
+        walk.next(p, g);
+        segs[sg % kSegs] = g;
+        mbar_arrive(bar(GFULL + sg % kSegs));
+        if (!g.valid) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ query loader, value tails
+    uint32_t ring = 0, tails = 0;
+    bool ok = true;
+    for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
+      const Seg g = seg_at(sg);
+      __syncwarp();
+      if (lane == 0) seg_done(sg);
+      const int n = g.i1 - g.i0;
+      if (!warp_wait(bar(QEMPTY), (sg & 1) ^ 1, abort_flag, p.ctl)) break;
+      constexpr int UPR = D / 8;
+      const int tile_rows = g.split ? kTile : kBlockRows;
+      const int64_t r0 = LIST ? 0 : static_cast<int64_t>(g.m) * kBlockRows;
+#pragma unroll 4
+      for (int x = lane; x < tile_rows * UPR; x += 32) {
+        const int r = x / UPR, u = x % UPR;
+        const bool in = r < g.rows;
+        const int64_t rr = r0 + (in ? r : 0);
+        const int64_t t = g.t0 + rr / p.G;
+        const int h = g.j * p.G + static_cast<int>(rr % p.G);
+        cp_async16(sQ + (r / kTile) * L::QTILE + (u / 8) * L::CHUNK + swz_offset(r % kTile, u % 8, 128),
+                   p.Q + (t * p.H + h) * D + u * 8, in ? 16u : 0u);
+      }
+      cp_async_mbar_arrive_noinc(bar(QFULL));
+      const int key0 = g.key0(g.i1 - 1);
+      if (!LIST && g.len > key0 && g.len < key0 + kTile) {
+        // the last tile's value rows past the end of the sequence
+        const uint32_t e = ring + v_at(n - 1, n), stage = e % ST;
+        ok = warp_wait(bar(VTAIL), tails & 1, abort_flag, p.ctl) &&
+             warp_wait(bar(FULL + stage), (e / ST) & 1, abort_flag, p.ctl);
+        if (!ok) break;
+        ++tails;
+        const int first = g.len - key0;
+        for (int x = lane; x < (kTile - first) * 8 * L::CH; x += 32) {
+          const int c = x / ((kTile - first) * 8), o = x % ((kTile - first) * 8);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                           sKV + stage * L::TILE + c * L::CHUNK + first * 128 + o * 16),
+                       "r"(0)
+                       : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(VREADY));
+      }
+      ring += 2 * n;
+    }
+  }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------ softmax and output
+    if constexpr (LIST) reg_inc<192>(); else reg_inc<216>();
+    const int slot = (warp - 4) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;  // TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tS = tmem_base + lanes + slot * kTile;
+    const uint32_t tO = tmem_base + lanes + 256 + slot * D;
+    uint32_t scount = 0, segs_split = 0, used = 0, used1 = 0;
+    bool ok = true;
+    for (; ok; ++sg) {
+      __syncwarp();
+      if (sg > 0 && lane == 0) seg_done(sg - 1);
+      if (!__all_sync(0xffffffffu, seg_wait(sg))) break;
+      const Seg& g = seg_at(sg);
+      const int n = g.tiles_of(slot);
+      const int r = (g.split ? 0 : slot * kTile) + row;  // row of the unit
+      const bool live = r < g.rows;
+      const bool warp_live = (r & ~31) < g.rows;
+      int pos;
+      if constexpr (LIST) {
+        pos = g.p0;
+      } else {
+        pos = live ? g.p0 + static_cast<int>((static_cast<int64_t>(g.m) * kBlockRows + r) / p.G) : -1;
+      }
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < n; ++i) {
+        const int x = g.i0 + (g.split ? 2 * i + slot : i);
+        uint32_t w[4];  // visible keys of the tile
+        if constexpr (LIST) {
+          const int cap = static_cast<int>(min(static_cast<int64_t>(p.max_blocks) << p.page_shift,
+                                               static_cast<int64_t>(0x7fffffff)));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int e = x * kTile + q * 32 + lane;
+            const int s = e < p.k ? __ldg(p.idx + static_cast<int64_t>(g.m) * p.k + e) : -1;
+            w[q] = __ballot_sync(0xffffffffu, s >= 0 && s <= pos && s < cap);
+          }
+        } else {
+          const int key0 = g.key0(x);
+          const int lim = pos - key0 + 1;  // keys of the tile at or before the query
+#pragma unroll
+          for (int q = 0; q < 4; ++q) w[q] = low_bits(lim - 32 * q);
+          if (p.window) {
+            const int lo = static_cast<int>(max(static_cast<int64_t>(lim) - p.window, static_cast<int64_t>(0)));
+            const int sk = max(p.sinks - key0, 0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) w[q] &= ~low_bits(lo - 32 * q) | low_bits(sk - 32 * q);
+          }
+        }
+        ok = warp_wait(bar(SFULL + slot), scount & 1, abort_flag, p.ctl);
+        if (!ok) break;
+        ++scount;
+        tc_fence_after();
+        if (warp_live) {
+          uint32_t v[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, v[q]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_wait_ld_regs(v[q]);
+          if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
+#pragma unroll
+            for (int q = 0; q < 128; ++q)
+              if (!((w[q >> 5] >> (q & 31)) & 1u)) v[q >> 5][q & 31] = 0xff800000u;  // -inf
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 128; q += 4)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(v[(q + y) >> 5][(q + y) & 31]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+          if (__any_sync(0xffffffffu, top > m + (i == 0 ? 0.0f : kRaise))) {
+            const bool raise = top > m + (i == 0 ? 0.0f : kRaise);
+            const float mn = raise ? top : m;
+            if (i > 0) {
+              // every earlier P V of this slot is done: S of this tile was issued after it
+              const float f = raise ? ex2(m - mn) : 1.0f;
+              l *= f;
+#pragma unroll
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + c0, o);
+                tmem_wait_ld_regs(o);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+                tmem_st16(tO + c0, o);
+              }
+            }
+            m = mn;
+          }
+          const float ref = m == -INFINITY ? 0.0f : m;
+          float2 sum = make_float2(0.0f, 0.0f);
+          const float2 cc = make_float2(p.c, p.c), nr = make_float2(-ref, -ref);
+#pragma unroll
+          for (int q0 = 0; q0 < 4; ++q0) {
+            uint32_t o[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float2 z = fma2(make_float2(__uint_as_float(v[q0][2 * q]),
+                                                __uint_as_float(v[q0][2 * q + 1])), cc, nr);
+              const float e0 = ex2(z.x), e1 = ex2(z.y);
+              sum.x += e0;
+              sum.y += e1;
+              o[q] = bf16x2(e0, e1);
+            }
+            tmem_st16(tS + q0 * 16, o);
+          }
+          l += sum.x + sum.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(PFULL + slot));
+      }
+      if (!ok) break;
+
+      // ---- the segment's result
+      const int64_t rr = (LIST ? 0 : static_cast<int64_t>(g.m) * kBlockRows) + r;
+      const int64_t t = g.t0 + rr / p.G;
+      const int h = g.j * p.G + static_cast<int>(rr % p.G);
+      const int64_t orow = t * p.H + h;
+      if (g.split && slot == 1) {
+        // (m, l) to slot 0, which joins the two halves of the tiles
+        ok = warp_wait(bar(MLEMPTY), (segs_split & 1) ^ 1, abort_flag, p.ctl);
+        if (!ok) break;
+        ml1[row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(MLFULL));
+        ++segs_split;
+        if (n > 0) ++used;
+        continue;
+      }
+      const int n1 = g.tiles_of(1);
+      float f0 = 1.0f, f1 = 0.0f;
+      if (g.split) {
+        ok = warp_wait(bar(MLFULL), segs_split & 1, abort_flag, p.ctl);
+        if (!ok) break;
+        ++segs_split;
+        const float2 o = ml1[row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(MLEMPTY));
+        const float mm = fmaxf(m, o.x);
+        const float ref = mm == -INFINITY ? 0.0f : mm;
+        f0 = ex2(m - ref);
+        f1 = ex2(o.x - ref);
+        l = l * f0 + (n1 > 0 ? o.y * f1 : 0.0f);
+        m = mm;
+      }
+      ok = warp_wait(bar(OFULL + slot), used & 1, abort_flag, p.ctl);
+      if (ok && g.split && n1 > 0) ok = warp_wait(bar(OFULL + 1), used1 & 1, abort_flag, p.ctl);
+      if (!ok) break;
+      ++used;
+      if (g.split ? n1 > 0 : true) ++used1;
+      tc_fence_after();
+      if (warp_live) {
+        const bool join = g.split && n1 > 0;
+        const float inv = g.part >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        const float a0 = f0 * inv, a1 = f1 * inv;
+        float* part_o = p.po + (static_cast<int64_t>(g.part) * kBlockRows + r) * D;
+        uint16_t* dst = p.out + orow * D;
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t v[32];
+          tmem_ld32(tO + c0, v);
+          tmem_wait_ld_regs(v);
+          float o[32];
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(v[q]) * a0;
+          if (join) {
+            tmem_ld32(tO + D + c0, v);
+            tmem_wait_ld_regs(v);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = fmaf(__uint_as_float(v[q]), a1, o[q]);
+          }
+          if (live) {
+            if (g.part >= 0) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4)
+                *reinterpret_cast<float4*>(part_o + c0 + q) =
+                    make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 32; q += 8)
+                *reinterpret_cast<uint4*>(dst + c0 + q) =
+                    make_uint4(bf16x2(o[q], o[q + 1]), bf16x2(o[q + 2], o[q + 3]),
+                               bf16x2(o[q + 4], o[q + 5]), bf16x2(o[q + 6], o[q + 7]));
+            }
+          }
+        }
+        if (live) {
+          if (g.part >= 0) {
+            *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(g.part) * kBlockRows + r) * 2) =
+                make_float2(m, l);
+          } else if (p.lse) {
+            p.lse[orow] = l > 0.0f ? (m + __log2f(l)) * 0.69314718055994530942f : l == 0.0f ? -INFINITY : l;
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(OEMPTY + slot));
+        if (g.split && n1 > 0) mbar_arrive(bar(OEMPTY + 1));
+      }
+    }
+  } else {
+    if constexpr (LIST) {
+      // -------------------------------------------------------- row loader of the list form
+      reg_dec<64>();
+      const int r = threadIdx.x - 384;  // entry of the tile
+      uint32_t ring = 0;
+      bool ok = true;
+      const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
+      for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
+        const Seg g = seg_at(sg);
+        __syncwarp();
+        if (lane == 0) seg_done(sg);
+        const int n = g.i1 - g.i0;
+        const int32_t* bt = p.bts + static_cast<int64_t>(g.b) * p.max_blocks;
+        const int32_t* list = p.idx + static_cast<int64_t>(g.m) * p.k;
+        auto entry = [&](int x) -> int {  // token of this thread's entry of tile x, or -1
+          const int64_t e = static_cast<int64_t>(g.i0 + x) * kTile + r;
+          return x < n && e < p.k ? __ldg(list + e) : -1;
+        };
+        auto phys = [&](int s) -> int64_t {  // cache row of token s, or -1: not visible
+          if (s < 0 || s > g.p0) return -1;
+          if (s >= cap) {
+            report(p.ctl, DEV_BAD_INPUT);
+            return -1;
+          }
+          int64_t pg = __ldg(bt + (s >> p.page_shift));
+          if (pg < 0 || pg >= p.n_pages) {
+            report(p.ctl, DEV_BAD_INPUT);
+            pg = 0;
+          }
+          return (pg << p.page_shift) | (s & ((1 << p.page_shift) - 1));
+        };
+        auto load = [&](const uint16_t* pool, uint32_t at, int64_t y) -> bool {
+          const uint32_t e = ring + at, stage = e % ST, phase = (e / ST) & 1;
+          if (!warp_wait(bar(EMPTY + stage), phase ^ 1, abort_flag, p.ctl)) return false;
+          const uint16_t* src = pool + ((y < 0 ? 0 : y) * p.Hkv + g.j) * D;
+          const uint32_t dst = sKV + stage * L::TILE;
+#pragma unroll
+          for (int u = 0; u < D / 8; ++u)
+            cp_async16(dst + (u / 8) * L::CHUNK + swz_offset(r, u % 8, 128), src + u * 8,
+                       y < 0 ? 0u : 16u);
+          cp_async_mbar_arrive_noinc(bar(FULL + stage));
+          return true;
+        };
+        int s_next = entry(1);
+        int64_t y_cur = phys(entry(0)), y_prev = -1;
+        for (int x = 0; x <= n && ok; ++x) {
+          const int s_after = entry(x + 2);
+          if (x < n) ok = load(p.kp, k_at(x), y_cur);
+          const int64_t y_next = phys(s_next);
+          if (ok && x > 0) ok = load(p.vp, v_at(x - 1, n), y_prev);
+          y_prev = y_cur;
+          y_cur = y_next;
+          s_next = s_after;
+        }
+        if (!ok) break;
+        ring += 2 * n;
+      }
+      cp_async_wait_all();
+    }
+  }
+
+  if (warp == 2) cp_async_wait_all();
+  __syncthreads();
+  if (*abort_flag) drain_pause(kDrainNs);  // let issued copies / MMAs land
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// Joins the parts of the unit that CTA blockIdx.x opened and did not finish:
+// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, parts in CTA order.  Each
+// warp takes a row at a time.
+template <int D, bool LIST>
+__global__ void __launch_bounds__(256) join_kernel(const AttParams p, int ctas) {
+  const int c = blockIdx.x;
+  const int4 open = p.head[2 * c + 1];
+  if (!open.x) return;
+  int64_t t0;
+  int rows;
+  if constexpr (LIST) {
+    if (open.z >= p.n_tok) return;
+    const int b = __ldg(p.seq_of + open.z);
+    if (b < 0 || b >= p.n_seq) return;
+    t0 = open.z;
+    rows = p.G;
+  } else {
+    const SeqInfo s = seq_info(p, open.y);
+    const Tiles t = unit_tiles(p, s, open.z);
+    t0 = s.t0;
+    rows = t.rows;
+  }
+  // the CTAs that follow, up to the one that ends the unit (a CTA whose share
+  // of it is less than a tile has no part)
+  int last = c;
+  for (int e = c + 1; e < ctas; ++e) {
+    const int4 cont = p.head[2 * e];
+    if (cont.x) last = e;
+    if (cont.y) break;
+  }
+  const int lane = lane_id();
+  for (int r = blockIdx.y * 8 + warp_id(); r < rows; r += gridDim.y * 8) {
+    float m = -INFINITY;
+    for (int e = c; e <= last; ++e) {
+      if (e > c && !p.head[2 * e].x) continue;
+      const int64_t q = static_cast<int64_t>(e == c ? 2 * e + 1 : 2 * e) * kBlockRows + r;
+      m = fmaxf(m, p.ml[2 * q]);
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
+    for (int e = c; e <= last; ++e) {
+      if (e > c && !p.head[2 * e].x) continue;
+      const int64_t q = static_cast<int64_t>(e == c ? 2 * e + 1 : 2 * e) * kBlockRows + r;
+      const float f = ex2(p.ml[2 * q] - ref);
+      l = fmaf(f, p.ml[2 * q + 1], l);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(f, p.po[q * D + i * 32 + lane], o[i]);
+    }
+    const int64_t rr = (LIST ? 0 : static_cast<int64_t>(open.z) * kBlockRows) + r;
+    const int64_t row = (t0 + rr / p.G) * p.H + open.w * p.G + rr % p.G;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      p.out[row * D + i * 32 + lane] =
+          static_cast<uint16_t>(bf16x2(o[i] * inv, 0.0f) & 0xffffu);
+    if (p.lse && lane == 0)
+      p.lse[row] = l > 0.0f ? (m + __log2f(l)) * 0.69314718055994530942f : l == 0.0f ? -INFINITY : l;
+  }
+}
+
+int att_ctas() { return sm_count(); }
+
+struct AttWs {
+  size_t head, ml, po, total;
+  explicit AttWs(int d) {
+    const size_t n = static_cast<size_t>(att_ctas());
+    size_t o = 0;
+    head = o;
+    o += (n * 2 * sizeof(int4) + 255) / 256 * 256;
+    ml = o;
+    o += n * 2 * kBlockRows * 2 * sizeof(float);
+    po = o;
+    o += n * 2 * kBlockRows * static_cast<size_t>(d) * sizeof(float);
+    total = o;
+  }
+};
+
+template <int D, bool LIST>
+cudaError_t launch_att(const AttParams& p, const CUtensorMap& km, const CUtensorMap& vm,
+                       cudaStream_t s) {
+  using L = AttLayout<D, LIST>;
+  auto kern = attend_kernel<D, LIST>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+  if (e != cudaSuccess) return e;
+  const int n = att_ctas();
+  kern<<<n, L::THREADS, L::ALLOC, s>>>(km, vm, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  join_kernel<D, LIST><<<dim3(n, 4), 256, 0, s>>>(p, n);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_workspace(int d) { return AttWs(d).total; }
+
+cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
+  AttParams p{};
+  p.Q = a.Q;
+  p.kp = a.k_pages;
+  p.vp = a.v_pages;
+  p.bts = a.block_tables;
+  p.cu_q = a.cu_q;
+  p.lens = a.seq_lens;
+  p.seq_of = a.seq_of;
+  p.positions = a.positions;
+  p.idx = a.idx;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.n_pages = a.n_pages;
+  p.key_rows = a.n_pages << a.page_shift;
+  p.max_blocks = a.max_blocks;
+  p.page_shift = a.page_shift;
+  p.n_seq = a.n_seq;
+  p.n_tok = a.n_tok;
+  p.H = a.H;
+  p.Hkv = a.Hkv;
+  p.G = a.H / a.Hkv;
+  p.window = a.window;
+  p.sinks = a.sinks;
+  p.k = a.k;
+  p.c = a.scale * 1.44269504088896340736f;
+  p.ctl = ctl;
+  const AttWs w(a.d);
+  uint8_t* base = static_cast<uint8_t*>(a.ws);
+  p.head = reinterpret_cast<int4*>(base + w.head);
+  p.ml = reinterpret_cast<float*>(base + w.ml);
+  p.po = reinterpret_cast<float*>(base + w.po);
+  CUtensorMap km, vm;
+  std::memset(&km, 0, sizeof km);
+  std::memset(&vm, 0, sizeof vm);
+  if (a.idx) return a.d == 128 ? launch_att<128, true>(p, km, vm, s) : launch_att<64, true>(p, km, vm, s);
+  const uint64_t dims[3] = {static_cast<uint64_t>(a.d), static_cast<uint64_t>(a.Hkv),
+                            static_cast<uint64_t>(p.key_rows)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(a.d) * 2,
+                               static_cast<uint64_t>(a.d) * 2 * static_cast<uint64_t>(a.Hkv)};
+  const uint32_t box[3] = {64, 1, 1u << a.page_shift};
+  if (encode_tensor_map(&km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.k_pages, dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tensor_map(&vm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.v_pages, dims, strides, box,
+                        CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return a.d == 128 ? launch_att<128, false>(p, km, vm, s) : launch_att<64, false>(p, km, vm, s);
+}
+
+}  // namespace misa

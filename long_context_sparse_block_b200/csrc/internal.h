@@ -115,6 +115,61 @@ cudaError_t launch_rerank_scores(const uint16_t* Q, const float* w, const void* 
                                  int H, int d, float* full, int64_t ldf, const DevCtl& ctl,
                                  cudaStream_t s);
 
+// Bookkeeping of a serving step (plan.cu).
+int plan_max_seq();
+cudaError_t launch_plan(const int32_t* q_lens, const int32_t* ctx_lens, int n_seq, int32_t* table,
+                        int max_blocks, int page_shift, int64_t n_pages, int n_tok,
+                        const int32_t* free_pages, int64_t free_cap, const int32_t* free_count,
+                        int32_t* cu_q, int32_t* seq_lens, int32_t* positions, int32_t* slots,
+                        int32_t* seq_of, int32_t* granted, int32_t* free_count_out,
+                        const DevCtl& ctl, cudaStream_t s);
+cudaError_t launch_release(const int32_t* release, int32_t* seq_lens, const int32_t* table,
+                           int n_seq, int max_blocks, int page_shift, int64_t n_pages,
+                           int32_t* free_pages, int64_t free_cap, int32_t* free_count,
+                           const DevCtl& ctl, cudaStream_t s);
+
+// Rotary positions (rope.cu): rows to rows, or to cache slots (slots != nullptr);
+// bf16 results at y, or e4m3 at y8 with a scale per row.
+struct RopeLaunch {
+  const uint16_t* x;         // [n, H, d]
+  const uint16_t* v;         // values copied beside the rows (v_pages), nullable
+  const int32_t* positions;
+  const int32_t* slots;
+  const double* inv_freq;
+  uint16_t* y;
+  uint8_t* y8;
+  float* scale;
+  uint16_t* v_pages;
+  int64_t rows_cap;          // rows of the page pool
+  int n, H, d, rope_dim, offset;
+  bool interleaved;
+  bool transpose;
+  float amplitude;
+};
+cudaError_t launch_rope(const RopeLaunch& a, const DevCtl& ctl, cudaStream_t s);
+
+// Attention over paged caches (attend.cu): over every visible key, or, with idx,
+// over each token's own list.
+struct AttendLaunch {
+  const uint16_t* Q;
+  const uint16_t* k_pages;
+  const uint16_t* v_pages;
+  const int32_t* block_tables;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  const int32_t* seq_of;     // list form
+  const int32_t* positions;  // list form
+  const int32_t* idx;        // list form: [n_tok, k]
+  uint16_t* out;
+  float* lse;
+  void* ws;
+  int64_t n_pages;
+  int n_tok, n_seq, max_blocks, page_shift, H, Hkv, d, window, sinks, k;
+  float scale;
+};
+size_t attend_workspace(int d);
+cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s);
+
 // Driver entry point for cuTensorMapEncodeTiled (resolved once).
 CUresult encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int rank,
                            const void* base, const uint64_t* dims, const uint64_t* strides_bytes,

@@ -1,0 +1,267 @@
+// Rotary positions of query and key rows, plain or quantised to e4m3 with a
+// scale per row, and the write of rotated keys (and of the values beside them)
+// into paged caches.
+//
+// A head row x of d elements keeps its elements outside [o, o + r); inside,
+// pair i < r / 2 is turned by the angle phi = pos * inv_freq[i] and scaled:
+//   (a, b) -> A * (a cos phi - b sin phi, a sin phi + b cos phi)
+// with a, b = x[o + 2i], x[o + 2i + 1] (interleaved) or x[o + i], x[o + r/2 + i]
+// (halves).  The transpose (the gradient of x given that of the result) is the
+// same with -phi.
+//
+// Angles: pos * inv_freq reaches 10^6 radians and more, where 32 bits leave
+// errors of 0.06; the product, and its reduction to a fraction of a turn, are
+// made in 64 bits, and sine and cosine of that fraction in 32 (errors near
+// 2^-24 of one).  They are computed once per (token, pair) into shared memory
+// and shared by the token's heads.
+//
+// What bounds it: a stream, 4 bytes per element for bf16 -> bf16 and 3 for
+// bf16 -> e4m3.  A thread moves 16-byte units (8 elements); the other half of a
+// pair of the halves layout lies in another lane of the same row and comes by a
+// shuffle, so every element is loaded once and rows may be rotated in place.
+// Rows are 4, 8 or 16 lanes (d = 32, 64, 128): row maxima stay in a warp.
+#include "internal.h"
+
+namespace misa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kUnits = 4;  // 16-byte units per thread, loaded together
+
+struct RopeParams {
+  const uint16_t* x;        // [n, H, d]
+  const uint16_t* v;        // [n, H, d] values to copy into v_pages, or nullptr
+  const int32_t* positions; // [n]
+  const int32_t* slots;     // [n] cache rows (paged writes), or nullptr
+  const double* inv_freq;   // [r / 2] radians per position
+  uint16_t* y;              // bf16 rows, or page rows
+  uint8_t* y8;              // e4m3 rows, or page rows
+  float* scale;             // e4m3: per row
+  uint16_t* v_pages;
+  int64_t rows_cap;         // rows of the page pool
+  int n;
+  int H;
+  int r;
+  int offset;
+  int tokens;               // tokens per CTA
+  int heads;                // heads per CTA
+  float amplitude;
+  float sign;               // -1: the transpose
+  DevCtl ctl;
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint16_t pack_e4m3(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// D: head size; PAIRED: interleaved layout; F8: e4m3 output; PAGED: rows go to
+// cache slots.  blockIdx.x: group of tokens, y: group of heads, z: 0 the rotated
+// rows, 1 the values (copied).
+template <int D, bool PAIRED, bool F8, bool PAGED>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  constexpr int UPR = D / 8;  // units (lanes) per head row
+  extern __shared__ float smem_cs[];  // [tokens][r]: cosines, then sines, of each token
+  const int t0 = blockIdx.x * p.tokens, h0 = blockIdx.y * p.heads;
+  const int nt = min(p.tokens, p.n - t0), nh = min(p.heads, p.H - h0);
+  const int half = p.r >> 1;
+  const int u = threadIdx.x % UPR;
+  const int rows = nt * nh;
+  constexpr int RPP = kRopeThreads / UPR;  // rows per pass
+  const bool values = PAGED && blockIdx.z == 1;
+  const uint16_t* src = values ? p.v : p.x;
+
+  // this thread's units, and where they go (-1: nowhere)
+  uint4 in[kUnits];
+  int64_t dst[kUnits];
+  int tok[kUnits];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    const int row = i * RPP + threadIdx.x / UPR;
+    dst[i] = -1;
+    tok[i] = 0;
+    in[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows) {
+      const int tl = row / nh, h = h0 + row - tl * nh, t = t0 + tl;
+      tok[i] = tl;
+      in[i] = *reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(t) * p.H + h) * D + u * 8);
+      int64_t out = t;
+      if constexpr (PAGED) {
+        out = __ldg(p.slots + t);
+        if (out >= p.rows_cap) {
+          report(p.ctl, DEV_BAD_INPUT);
+          out = -1;
+        }
+      } else if (__ldg(p.positions + t) < 0) {
+        out = -1;  // a row of no sequence: left as it was
+      }
+      if (out >= 0) dst[i] = out * p.H + h;
+    }
+  }
+  if (values) {
+    if constexpr (PAGED) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+        if (dst[i] >= 0) *reinterpret_cast<uint4*>(p.v_pages + dst[i] * D + u * 8) = in[i];
+    }
+    return;
+  }
+
+  for (int x = threadIdx.x; x < nt * half; x += kRopeThreads) {
+    const int tl = x / half, i = x - tl * half;
+    const double turns =
+        static_cast<double>(__ldg(p.positions + t0 + tl)) * (__ldg(p.inv_freq + i) * 0.15915494309189533577);
+    const float frac = static_cast<float>(turns - rint(turns));
+    float sn, cs;
+    sincospif(2.0f * frac, &sn, &cs);
+    smem_cs[tl * p.r + i] = p.amplitude * cs;
+    smem_cs[tl * p.r + half + i] = p.sign * p.amplitude * sn;
+  }
+  __syncthreads();
+
+  const int first = p.offset >> 3, units = p.r >> 3;  // rotated units of a row
+  const bool turned = u >= first && u < first + units;
+  const int lane = lane_id();
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) {
+    float e[8] = {bf_lo(in[i].x), bf_hi(in[i].x), bf_lo(in[i].y), bf_hi(in[i].y),
+                  bf_lo(in[i].z), bf_hi(in[i].z), bf_lo(in[i].w), bf_hi(in[i].w)};
+    const float* cs = smem_cs + tok[i] * p.r;
+    if constexpr (PAIRED) {
+      if (turned) {
+        const int pi = (u - first) * 4;
+        const float4 c = *reinterpret_cast<const float4*>(cs + pi);
+        const float4 s = *reinterpret_cast<const float4*>(cs + half + pi);
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = e[2 * j], b = e[2 * j + 1];
+          e[2 * j] = a * cc[j] - b * ss[j];
+          e[2 * j + 1] = a * ss[j] + b * cc[j];
+        }
+      }
+    } else {
+      // the other half of each pair: units / 2 lanes up or down in the same row
+      const bool low = u - first < (units >> 1);
+      const int other = turned ? lane + (low ? (units >> 1) : -(units >> 1)) : lane;
+      uint4 o;
+      o.x = __shfl_sync(0xffffffffu, in[i].x, other);
+      o.y = __shfl_sync(0xffffffffu, in[i].y, other);
+      o.z = __shfl_sync(0xffffffffu, in[i].z, other);
+      o.w = __shfl_sync(0xffffffffu, in[i].w, other);
+      if (turned) {
+        const float f[8] = {bf_lo(o.x), bf_hi(o.x), bf_lo(o.y), bf_hi(o.y),
+                            bf_lo(o.z), bf_hi(o.z), bf_lo(o.w), bf_hi(o.w)};
+        const int pi = (u - first - (low ? 0 : (units >> 1))) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          const float4 c = *reinterpret_cast<const float4*>(cs + pi + j);
+          const float4 s = *reinterpret_cast<const float4*>(cs + half + pi + j);
+          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            e[j + q] = low ? e[j + q] * cc[q] - f[j + q] * ss[q] : f[j + q] * ss[q] + e[j + q] * cc[q];
+        }
+      }
+    }
+    if constexpr (F8) {
+      // scale = largest magnitude / 448 (1 for a row of zeros); codes rounded to
+      // nearest even from the 32-bit rotated values
+      float m = 0.0f;
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m = fmaxf(m, fabsf(e[j]));
+        bad = bad || !(fabsf(e[j]) <= 3.402823466e38f);
+      }
+#pragma unroll
+      for (int o = 1; o < UPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float scale = m / 448.0f;
+      if (scale == 0.0f) scale = 1.0f;  // a row of zeros, or too small to have a scale
+      if (dst[i] >= 0) {
+        if (bad) report(p.ctl, DEV_BAD_INPUT);
+        uint2 w;
+        const uint32_t q0 = pack_e4m3(e[0] / scale, e[1] / scale);
+        const uint32_t q1 = pack_e4m3(e[2] / scale, e[3] / scale);
+        const uint32_t q2 = pack_e4m3(e[4] / scale, e[5] / scale);
+        const uint32_t q3 = pack_e4m3(e[6] / scale, e[7] / scale);
+        w.x = q0 | (q1 << 16);
+        w.y = q2 | (q3 << 16);
+        *reinterpret_cast<uint2*>(p.y8 + dst[i] * D + u * 8) = w;
+        if (u == 0) p.scale[dst[i]] = scale;
+      }
+    } else {
+      if (dst[i] >= 0) {
+        uint4 w;
+        w.x = pack_bf16(e[0], e[1]);
+        w.y = pack_bf16(e[2], e[3]);
+        w.z = pack_bf16(e[4], e[5]);
+        w.w = pack_bf16(e[6], e[7]);
+        *reinterpret_cast<uint4*>(p.y + dst[i] * D + u * 8) = w;
+      }
+    }
+  }
+}
+
+template <int D, bool PAIRED, bool F8, bool PAGED>
+cudaError_t launch_one(RopeParams p, cudaStream_t s) {
+  // as many heads of a token as the CTA holds, then as many tokens
+  constexpr int ROWS = kUnits * kRopeThreads / (D / 8);
+  p.heads = p.H < ROWS ? p.H : ROWS;
+  p.tokens = ROWS / p.heads;
+  const int smem = p.tokens * p.r * static_cast<int>(sizeof(float));
+  static_assert(ROWS * D * 4 <= 48 * 1024, "a row's cosines and sines per row of the CTA");
+  const dim3 grid((p.n + p.tokens - 1) / p.tokens, (p.H + p.heads - 1) / p.heads, p.v ? 2 : 1);
+  rope_kernel<D, PAIRED, F8, PAGED><<<grid, kRopeThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const RopeParams& p, bool interleaved, cudaStream_t s) {
+  const bool f8 = p.y8 != nullptr, paged = p.slots != nullptr;
+  if (interleaved) {
+    if (f8) return paged ? launch_one<D, true, true, true>(p, s) : launch_one<D, true, true, false>(p, s);
+    return paged ? launch_one<D, true, false, true>(p, s) : launch_one<D, true, false, false>(p, s);
+  }
+  if (f8) return paged ? launch_one<D, false, true, true>(p, s) : launch_one<D, false, true, false>(p, s);
+  return paged ? launch_one<D, false, false, true>(p, s) : launch_one<D, false, false, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeLaunch& a, const DevCtl& ctl, cudaStream_t s) {
+  RopeParams p{};
+  p.x = a.x;
+  p.v = a.v;
+  p.positions = a.positions;
+  p.slots = a.slots;
+  p.inv_freq = a.inv_freq;
+  p.y = a.y;
+  p.y8 = a.y8;
+  p.scale = a.scale;
+  p.v_pages = a.v_pages;
+  p.rows_cap = a.rows_cap;
+  p.n = a.n;
+  p.H = a.H;
+  p.r = a.rope_dim;
+  p.offset = a.offset;
+  p.amplitude = a.amplitude;
+  p.sign = a.transpose ? -1.0f : 1.0f;
+  p.ctl = ctl;
+  switch (a.d) {
+    case 32: return launch_d<32>(p, a.interleaved, s);
+    case 64: return launch_d<64>(p, a.interleaved, s);
+    case 128: return launch_d<128>(p, a.interleaved, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace misa

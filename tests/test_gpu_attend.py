@@ -1,0 +1,296 @@
+"""Attention over paged caches, and over selected tokens, against the formulas in 64
+bits (tests/serving_helpers.py has the references and derives the tolerances)."""
+import numpy as np
+import pytest
+import torch
+
+from tests.serving_helpers import Cache, check_rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from long_context_sparse_block_b200 import _lib
+    return _lib
+
+
+def _batch(q_lens, lens, H, Hkv, d, page, seed, pad=0):
+    """Packed queries of sequences with lens[b] keys, q_lens[b] of them new."""
+    cache = Cache(lens, Hkv, d, page, seed)
+    cu = np.concatenate([[0], np.cumsum(q_lens)]).astype(np.int32)
+    n_tok = int(cu[-1]) + pad
+    g = torch.Generator().manual_seed(seed + 1)
+    Q = (1.5 * torch.randn((n_tok, H, d), generator=g)).to(torch.bfloat16)
+    seqs = np.repeat(np.arange(len(lens)), q_lens)
+    pos = np.concatenate([np.arange(n - q, n) for q, n in zip(q_lens, lens)] or [[]]).astype(np.int64)
+    i32 = lambda x: torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device="cuda")
+    return cache, Q.cuda(), i32(cu), i32(lens), seqs, pos
+
+
+def _run(lib, cache, Q, cu, lens, **kw):
+    out = torch.full_like(Q, 7.0)
+    lse = torch.full(Q.shape[:2], 7.0, dtype=torch.float32, device="cuda")
+    ws = torch.full((lib.misa_workspace_size("attend", 1, 0, Q.shape[2], 0),), 255, dtype=torch.uint8,
+                    device="cuda")   # NaN patterns: nothing may be read before it is written
+    lib.misa_attend_paged(Q, cache.k_pages, cache.v_pages, cache.table, cu, lens, out=out, lse=lse,
+                          ws=ws, **kw)
+    torch.cuda.synchronize()
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    return out, lse
+
+
+def _sample(n, most=24, seed=0):
+    if n <= most:
+        return list(range(n))
+    rng = np.random.Generator(np.random.PCG64(seed))
+    return sorted(set([0, 1, n - 2, n - 1]) | set(rng.integers(0, n, most).tolist()))
+
+
+@pytest.mark.parametrize("H,Hkv,d,page,q_lens,lens", [
+    (8, 1, 128, 64, [1], [1]),                               # one token, one key
+    (8, 1, 128, 64, [1], [129]),
+    (8, 2, 128, 16, [1, 1, 1], [1, 127, 128]),               # single tokens around a tile
+    (16, 2, 64, 32, [1, 1, 1, 1], [5, 300, 1000, 2049]),
+    (64, 8, 128, 64, [1] * 5, [700, 1, 64, 4097, 130]),
+    (4, 4, 128, 128, [3, 0, 5], [3, 77, 260]),               # no grouping, an empty request
+    (6, 2, 128, 16, [33, 1, 70], [33, 500, 200]),            # groups of 3
+    (14, 2, 64, 64, [40], [171]),                            # groups of 7
+    (32, 4, 128, 64, [64], [1000]),                          # two 256-row blocks
+    (8, 1, 64, 64, [300], [300]),                            # a whole prompt
+    (12, 4, 128, 32, [257, 31], [600, 31]),                  # ragged row blocks
+    (128, 1, 128, 64, [3], [515]),                           # the largest group
+    (1, 1, 64, 16, [129], [400]),                            # a single head
+])
+def test_attend_matches_the_formula(lib, H, Hkv, d, page, q_lens, lens):
+    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, H, Hkv, d, page, seed=3)
+    out, lse = _run(lib, cache, Q, cu, ln)
+    check_rows(out, lse, _sample(len(seqs)), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), H // Hkv,
+               d ** -0.5)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 4), (100, 0), (128, 130), (300, 4),
+                                          (5000, 9)])
+@pytest.mark.parametrize("H,Hkv,d,page,q_lens,lens", [
+    (8, 2, 128, 64, [1, 1, 1], [900, 50, 257]),
+    (8, 2, 64, 16, [200, 3], [700, 3]),
+])
+def test_attend_window_and_first_tokens(lib, window, sinks, H, Hkv, d, page, q_lens, lens):
+    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, H, Hkv, d, page, seed=5)
+    out, lse = _run(lib, cache, Q, cu, ln, window=window, sinks=sinks)
+
+    def sees(t):
+        s = np.arange(pos[t] + 1)
+        return s[(s > pos[t] - window) | (s < sinks)]
+    check_rows(out, lse, _sample(len(seqs), 16), Q, cache, seqs, sees, H // Hkv, d ** -0.5)
+
+
+def test_attend_long_contexts_are_split_and_joined(lib):
+    # few rows over long caches: every unit is cut into parts by many CTAs
+    q_lens, lens = [1, 2, 1], [40000, 9000, 12345]
+    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, 8, 2, 128, 64, seed=7)
+    out, lse = _run(lib, cache, Q, cu, ln)
+    check_rows(out, lse, range(4), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 4, 128 ** -0.5)
+    again = _run(lib, cache, Q, cu, ln)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_attend_many_short_sequences(lib):
+    rng = np.random.Generator(np.random.PCG64(11))
+    n = 700                                    # more sequences than a CTA has threads
+    q_lens = rng.integers(0, 4, n).tolist()
+    lens = [q + int(x) for q, x in zip(q_lens, rng.integers(0, 90, n))]
+    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, 4, 2, 64, 16, seed=12)
+    out, lse = _run(lib, cache, Q, cu, ln)
+    check_rows(out, lse, _sample(len(seqs), 120), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 2,
+               64 ** -0.5)
+
+
+def test_attend_scores_that_keep_growing(lib):
+    # every later tile raises the running reference: the rescaling path
+    cache, Q, cu, ln, seqs, pos = _batch([2], [1500], 8, 1, 128, 64, seed=13)
+    gain = torch.linspace(0.1, 12.0, 1500).to(torch.bfloat16)
+    q0 = Q[0, 0].cpu().float()
+    for s in range(1500):
+        cache.K[0][s, 0] = (cache.K[0][s, 0].float() * 0.1 + gain[s].float() * q0 / q0.norm() * 3).to(
+            torch.bfloat16)
+        pg = int(cache.table[0, s // 64])
+        cache.k_pages[pg, s % 64, 0] = cache.K[0][s, 0].cuda()
+    Q[:, :] = Q[0, 0]
+    Q[1] *= -1.0                                # and one row whose scores fall
+    out, lse = _run(lib, cache, Q, cu, ln)
+    check_rows(out, lse, range(2), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 8, 128 ** -0.5)
+
+
+def test_attend_rows_that_see_nothing_and_rows_behind(lib):
+    # a refused request (no keys) gives zeros; rows past the last sequence stay
+    cache, Q, cu, ln, seqs, pos = _batch([3, 2], [10, 40], 8, 2, 128, 16, seed=17, pad=5)
+    ln[0] = 0
+    out, lse = _run(lib, cache, Q, cu, ln)
+    assert torch.equal(out[:3], torch.zeros_like(out[:3]))
+    assert torch.isinf(lse[:3]).all() and (lse[:3] < 0).all()
+    assert (out[5:] == 7.0).all() and (lse[5:] == 7.0).all()
+    check_rows(out, lse, [3, 4], Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 4, 128 ** -0.5)
+    ln[0] = 2                                   # the first new token sees nothing, the others do
+    out, lse = _run(lib, cache, Q, cu, ln)
+    assert torch.equal(out[0], torch.zeros_like(out[0])) and torch.isinf(lse[0]).all()
+    check_rows(out, lse, [1, 2], Q, cache, seqs, lambda t: slice(0, t), 4, 128 ** -0.5)
+
+
+def test_attend_reports_bad_pages_and_lengths(lib):
+    cache, Q, cu, ln, seqs, pos = _batch([1], [100], 4, 1, 64, 16, seed=19)
+    bad = cache.table.clone()
+    bad[0, 2] = cache.n_pages + 5
+    kp = torch.nan_to_num(cache.k_pages)
+    vp = torch.nan_to_num(cache.v_pages)
+    lib.misa_attend_paged(Q, kp, vp, bad, cu, ln)
+    assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+    lib.misa_attend_paged(Q, kp, vp, cache.table, cu, ln + 1000)      # past the table
+    assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+    out, _ = lib.misa_attend_paged(Q, kp, vp, cache.table, cu, ln)
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    check_rows(out, None, [0], Q, cache, seqs, lambda t: slice(0, 100), 4, 64 ** -0.5)
+
+
+# ------------------------------------------------------------------ selected tokens
+
+def _lists(pos, k, seed, shuffle=False):
+    rng = np.random.Generator(np.random.PCG64(seed))
+    idx = np.full((len(pos), k), -1, dtype=np.int32)
+    for t, p in enumerate(pos):
+        n = min(k, int(p) + 1)
+        pick = rng.choice(int(p) + 1, size=n, replace=False)
+        pick = rng.permutation(pick) if shuffle else np.sort(pick)
+        at = np.sort(rng.choice(k, size=n, replace=False)) if shuffle else np.arange(n)
+        idx[t, at] = pick
+    return idx
+
+
+def _run_selected(lib, cache, Q, seq_of, pos, idx, **kw):
+    out = torch.full_like(Q, 7.0)
+    lse = torch.full(Q.shape[:2], 7.0, dtype=torch.float32, device="cuda")
+    ws = torch.full((lib.misa_workspace_size("attend", 1, 0, Q.shape[2], 0),), 255, dtype=torch.uint8,
+                    device="cuda")
+    lib.misa_attend_selected(Q, cache.k_pages, cache.v_pages, cache.table, seq_of, pos, idx, out=out,
+                             lse=lse, ws=ws, **kw)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("shuffle", [False, True])
+@pytest.mark.parametrize("H,Hkv,d,page,q_lens,lens,k", [
+    (64, 1, 128, 64, [1, 1, 1], [5000, 100, 1], 256),
+    (8, 1, 128, 64, [1], [4000], 1),
+    (128, 1, 128, 16, [5], [900], 129),
+    (24, 4, 64, 32, [7, 0, 9], [40, 10, 700], 333),
+    (6, 2, 128, 128, [40], [40], 64),             # most rows see fewer tokens than k
+    (16, 1, 64, 64, [300], [1000], 100),          # more units than CTAs
+])
+def test_selected_matches_the_formula(lib, shuffle, H, Hkv, d, page, q_lens, lens, k):
+    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, H, Hkv, d, page, seed=23)
+    idx = _lists(pos, k, 29, shuffle)
+    i32 = lambda x: torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device="cuda")
+    out, lse = _run_selected(lib, cache, Q, i32(seqs), i32(pos), i32(idx))
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    check_rows(out, lse, _sample(len(seqs)), Q, cache, seqs,
+               lambda t: idx[t][idx[t] >= 0].astype(np.int64), H // Hkv, d ** -0.5)
+
+
+def test_selected_ignores_what_a_row_may_not_see(lib):
+    # tokens past the position, negative entries, an empty list, a row of no sequence;
+    # a token listed twice counts twice
+    cache, Q, cu, ln, seqs, pos = _batch([5], [300], 8, 1, 128, 64, seed=31)
+    i32 = lambda x: torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device="cuda")
+    idx = np.full((5, 140), -1, dtype=np.int32)
+    idx[0, :4] = [3, 299, 7, 298]                 # row 0 sits at 295
+    idx[1, 130:134] = [10, 20, -7, 10]
+    idx[2] = -1
+    idx[3, :2] = [299, 5]
+    idx[4] = np.arange(140)
+    seq_of = np.array([0, 0, 0, -1, 0])
+    out, lse = _run_selected(lib, cache, Q, i32(seq_of), i32(pos), i32(idx))
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    want = {0: [3, 7], 1: [10, 20, 10], 4: list(range(140))}
+    check_rows(out, lse, [0, 1, 4], Q, cache, seqs, lambda t: np.array(want[t]), 8, 128 ** -0.5)
+    assert torch.equal(out[2], torch.zeros_like(out[2])) and torch.isinf(lse[2]).all()
+    assert (out[3] == 7.0).all() and (lse[3] == 7.0).all()
+
+
+def test_selected_reports_sequences_and_tokens_out_of_range(lib):
+    cache, Q, cu, ln, seqs, pos = _batch([2], [40], 4, 1, 64, 16, seed=37)
+    i32 = lambda x: torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device="cuda")
+    idx = i32([[1, 2], [3, 39]])
+    out, _ = _run_selected(lib, cache, Q, i32([0, 1]), i32(pos), idx)       # one sequence only
+    assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+    assert (out[1] == 7.0).all()
+    far = i32([[1, 48], [3, 39]])                                            # 3 pages of 16
+    out, _ = _run_selected(lib, cache, Q, i32([0, 0]), i32([100, 39]), far)
+    assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+    check_rows(out, None, [0], Q, cache, seqs, lambda t: np.array([1]), 4, 64 ** -0.5)
+
+
+def test_selected_of_everything_equals_attend(lib):
+    cache, Q, cu, ln, seqs, pos = _batch([4], [500], 16, 2, 128, 64, seed=41)
+    i32 = lambda x: torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device="cuda")
+    idx = np.tile(np.arange(500, dtype=np.int32), (4, 1))
+    out, lse = _run_selected(lib, cache, Q, i32(seqs), i32(pos), i32(idx))
+    full, flse = _run(lib, cache, Q, cu, ln)
+    rows = range(4)
+    for o, l in ((out, lse), (full, flse)):
+        check_rows(o, l, rows, Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 8, 128 ** -0.5)
+
+
+# ------------------------------------------------------------------ streams, graphs, waits
+
+def test_attend_in_a_graph_and_beside_another_stream(lib):
+    cache, Q, cu, ln, seqs, pos = _batch([1, 1, 4], [700, 2000, 300], 16, 2, 128, 64, seed=43)
+    ref, rlse = _run(lib, cache, Q, cu, ln)
+    out, lse = torch.empty_like(ref), torch.empty_like(rlse)
+    ws = [torch.empty(lib.misa_workspace_size("attend", 1, 0, 128, 0), dtype=torch.uint8, device="cuda")
+          for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        lib.misa_attend_paged(Q, cache.k_pages, cache.v_pages, cache.table, cu, ln, out=out, lse=lse,
+                              ws=ws[0])
+    other = torch.cuda.Stream()
+    for _ in range(5):
+        out.zero_()
+        other.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        with torch.cuda.stream(other):           # its own workspace: the calls may overlap
+            o2, l2 = lib.misa_attend_paged(Q, cache.k_pages, cache.v_pages, cache.table, cu, ln,
+                                           want_lse=True, ws=ws[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(lse, rlse)
+        assert torch.equal(o2, ref) and torch.equal(l2, rlse)
+    # the replay reads the lengths of its time
+    ln[1] = 900
+    graph.replay()
+    torch.cuda.synchronize()
+    sees = lambda t: slice(0, (900 if t == 1 else pos[t] + 1))
+    check_rows(out, lse, [0, 1], Q, cache, seqs, sees, 8, 128 ** -0.5)
+
+
+def test_expired_waits_report_timeout(lib):
+    cache, Q, cu, ln, seqs, pos = _batch([1] * 8, [3000] * 8, 16, 2, 128, 64, seed=47)
+    ref, rlse = _run(lib, cache, Q, cu, ln)
+    i32 = lambda x: torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device="cuda")
+    idx = i32(_lists(pos, 512, 3))
+    sref, slse = _run_selected(lib, cache, Q, i32(seqs), i32(pos), idx)
+    try:
+        for sel in (False, True):
+            lib.misa_set_wait_limit_ns(1)
+            if sel:
+                lib.misa_attend_selected(Q, cache.k_pages, cache.v_pages, cache.table, i32(seqs),
+                                         i32(pos), idx)
+            else:
+                lib.misa_attend_paged(Q, cache.k_pages, cache.v_pages, cache.table, cu, ln)
+            assert lib.misa_last_device_status() == lib.MISA_ERR_TIMEOUT
+            lib.misa_set_wait_limit_ns(0)
+    finally:
+        lib.misa_set_wait_limit_ns(0)
+    out, lse = _run(lib, cache, Q, cu, ln)
+    assert torch.equal(out, ref) and torch.equal(lse, rlse)
+    out, lse = _run_selected(lib, cache, Q, i32(seqs), i32(pos), idx)
+    assert torch.equal(out, sref) and torch.equal(lse, slse)

@@ -1,0 +1,298 @@
+"""Rotary positions, cache appends and step plans against their formulas."""
+import numpy as np
+import pytest
+import torch
+
+from tests.serving_helpers import rotated
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from long_context_sparse_block_b200 import _lib
+    return _lib
+
+
+def _rows(n, H, d, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn((n, H, d), generator=g).to(torch.bfloat16)
+
+
+def _freqs(lib, r, seed):
+    if seed % 2:
+        return lib.misa_rope_frequencies(r, scaling="bands", factor=40.0)
+    return lib.misa_rope_frequencies(r)
+
+
+ROPE = [  # n, H, d, r, offset, interleaved
+    (1, 1, 32, 16, 0, False), (1, 64, 128, 64, 0, True), (3, 5, 64, 64, 0, False),
+    (7, 3, 64, 32, 32, True), (65, 8, 128, 64, 64, False), (130, 1, 128, 128, 0, True),
+    (33, 70, 32, 32, 0, False), (20, 130, 64, 16, 24, False), (9, 2, 128, 48, 8, True),
+    (9, 2, 128, 48, 8, False), (9, 2, 128, 96, 16, False),
+]
+
+
+@pytest.mark.parametrize("n,H,d,r,offset,interleaved", ROPE)
+@pytest.mark.parametrize("transpose", [False, True])
+def test_rope_matches_the_formula(lib, n, H, d, r, offset, interleaved, transpose):
+    x = _rows(n, H, d, n + H)
+    f, amp = _freqs(lib, r, n)
+    pos = np.random.Generator(np.random.PCG64(n)).integers(0, 1 << 21, n)
+    want, mag = rotated(x.float().numpy(), pos, f.cpu().numpy(), offset, interleaved, amp, transpose)
+    p = torch.as_tensor(pos, dtype=torch.int32, device="cuda")
+    y = lib.misa_rope(x.cuda(), p, f, offset=offset, interleaved=interleaved, amplitude=amp,
+                      transpose=transpose)
+    got = y.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= 2.0 ** -21 * mag + 2.0 ** -8 * np.abs(want))
+    keep = np.ones(d, dtype=bool)
+    keep[offset:offset + r] = False
+    assert np.array_equal(got[..., keep], x.double().numpy()[..., keep])
+    inplace = x.cuda()
+    assert lib.misa_rope(inplace, p, f, offset=offset, interleaved=interleaved, amplitude=amp,
+                         transpose=transpose, out=inplace) is inplace
+    assert torch.equal(inplace, y)
+
+
+def test_rope_far_positions_and_rows_of_no_sequence(lib):
+    x = _rows(4, 2, 64, 1)
+    f, amp = lib.misa_rope_frequencies(64)
+    pos = np.array([2**31 - 1, -1, 123456789, 0])
+    # the angle itself: 2^31 radians in fp64 is off by 2^-53 2^31, far below the fp32 sine's 2^-22
+    want, mag = rotated(x.float().numpy(), pos, f.cpu().numpy(), 0, False, amp)
+    out = torch.full_like(x, 7.0).cuda()
+    lib.misa_rope(x.cuda(), torch.as_tensor(pos, dtype=torch.int32, device="cuda"), f, out=out)
+    got = out.double().cpu().numpy()
+    live = [0, 2, 3]
+    assert np.all(np.abs(got - want)[live] <= 2.0 ** -21 * mag[live] + 2.0 ** -8 * np.abs(want)[live])
+    assert np.all(got[1] == 7.0)
+    assert np.array_equal(got[3], x.double().numpy()[3])        # position 0: unchanged
+
+
+def test_rope_transpose_is_the_gradient(lib):
+    # <g, R x> = <R^T g, x> for the formula, and R^T g by differences of the kernel's own R
+    n, H, d, r = 5, 3, 64, 32
+    f, amp = lib.misa_rope_frequencies(r, scaling="bands", factor=8.0)
+    pos = torch.tensor([0, 1, 77, 4096, 100000], dtype=torch.int32, device="cuda")
+    g = _rows(n, H, d, 2).cuda()
+    back = lib.misa_rope(g, pos, f, offset=16, interleaved=True, amplitude=amp, transpose=True).double()
+    unit = torch.zeros((n, H, d), dtype=torch.bfloat16, device="cuda")
+    for e in (0, 16, 17, 30, 47, 63):
+        unit.zero_()
+        unit[..., e] = 1.0
+        # R is linear: its difference along a unit step is R applied to the step
+        col = lib.misa_rope(unit, pos, f, offset=16, interleaved=True, amplitude=amp).double()
+        want = (g.double() * col).sum(-1)
+        # both sides are rounded to bf16 once: half a step of two entries of R (each at most
+        # amp, times |g|) and of the result, and the rotation's own 2^-21 A (|a| + |b|)
+        big = g.double().abs().amax(-1) * amp
+        assert bool(((back[..., e] - want).abs() <= 2.0 ** -8 * (2 * big + want.abs()) + 2.0 ** -19 * big).all())
+
+
+@pytest.mark.parametrize("n,H,d,r,offset,interleaved", ROPE)
+def test_rope_fp8_codes_and_scales(lib, n, H, d, r, offset, interleaved):
+    x = _rows(n, H, d, n + H + 1)
+    x[0, 0] = 0
+    f, amp = _freqs(lib, r, n)
+    pos = np.random.Generator(np.random.PCG64(n)).integers(0, 1 << 20, n)
+    want, mag = rotated(x.float().numpy(), pos, f.cpu().numpy(), offset, interleaved, amp)
+    codes, scale = lib.misa_rope_fp8(x.cuda(), torch.as_tensor(pos, dtype=torch.int32, device="cuda"), f,
+                                     offset=offset, interleaved=interleaved, amplitude=amp)
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    top = np.abs(want).max(-1)
+    err = (2.0 ** -21 * mag).max(-1)
+    s = scale.double().cpu().numpy()
+    assert np.all(np.abs(s - np.where(top > 0, top / 448, 1.0)) <= err / 448 + 2.0 ** -23 * top / 448)
+    val = codes.view(torch.float8_e4m3fn).double().cpu().numpy() * s[..., None]
+    # half a step of e4m3: 2^-4 of the value, or half of its smallest step 2^-9 (in scales)
+    tol = np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10 * s[..., None]) + 1.125 * 2.0 ** -21 * mag + \
+        2.0 ** -20 * np.abs(want)
+    assert np.all(np.abs(val - want) <= tol)
+
+
+@pytest.mark.parametrize("form", ["kv", "index", "index_bf16"])
+@pytest.mark.parametrize("page", [16, 128])
+def test_cache_append(lib, form, page):
+    n, H, d, r = 37, 1 if form != "kv" else 4, 128, 64
+    x, v = _rows(n, H, d, 5), _rows(n, H, d, 6)
+    f, amp = lib.misa_rope_frequencies(r)
+    n_pages = -(-n // page) + 2
+    rng = np.random.Generator(np.random.PCG64(3))
+    slots = rng.permutation(n_pages * page)[:n].astype(np.int32)
+    slots[5] = -1
+    pos = np.arange(n) + 1000
+    want, mag = rotated(x.float().numpy(), pos, f.cpu().numpy(), 64, False, amp)
+    i32 = lambda a: torch.as_tensor(a, dtype=torch.int32, device="cuda")
+    live = slots >= 0
+    at = slots[live]
+    rest = np.ones(n_pages * page, dtype=bool)
+    rest[at] = False
+    if form == "index":
+        kp = torch.full((n_pages, page, d), 0x7E, dtype=torch.uint8, device="cuda")
+        ks = torch.full((n_pages, page), -3.0, device="cuda")
+        lib.misa_cache_append(x[:, 0].contiguous().cuda(), i32(pos), i32(slots), f, kp, k_scale=ks, offset=64)
+        codes, scale = lib.misa_rope_fp8(x.cuda(), i32(pos), f, offset=64)
+        assert torch.equal(kp.view(-1, d)[i32(at).long()], codes[live, 0])
+        assert torch.equal(ks.view(-1)[i32(at).long()], scale[live, 0])
+        assert bool((kp.view(-1, d)[torch.from_numpy(rest).cuda()] == 0x7E).all())
+        assert bool((ks.view(-1)[torch.from_numpy(rest).cuda()] == -3.0).all())
+    else:
+        shape = (n_pages, page, H, d) if form == "kv" else (n_pages, page, d)
+        kp = torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        vp = torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda") if form == "kv" else None
+        xx = x.cuda() if form == "kv" else x[:, 0].contiguous().cuda()
+        lib.misa_cache_append(xx, i32(pos), i32(slots), f, kp, offset=64,
+                              v=v.cuda() if form == "kv" else None, v_pages=vp)
+        got = kp.view(-1, H, d).double().cpu().numpy()
+        assert np.all(np.abs(got[at] - want[live]) <= 2.0 ** -21 * mag[live] + 2.0 ** -8 * np.abs(want[live]))
+        assert np.all(got[rest] == 7.0)
+        if form == "kv":
+            gv = vp.view(-1, H, d).cpu()
+            assert torch.equal(gv[torch.from_numpy(at).long()], v[live])
+            assert bool((gv[torch.from_numpy(rest)] == 7.0).all())
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    if form == "kv":                              # a slot past the pool is skipped and reported
+        slots[7] = n_pages * page
+        lib.misa_cache_append(x.cuda(), i32(pos), i32(slots), f, kp, offset=64)
+        assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+
+
+# ------------------------------------------------------------------ step plans
+
+def plan_reference(q, ctx, table, page, n_tok, free, count):
+    """The plan in plain Python; table is changed in place."""
+    n, width = table.shape
+    cu, at, taken, out_of = [0], 0, 0, False
+    pos, slots, seq = [np.full(n_tok, -1, dtype=np.int64) for _ in range(3)]
+    lens, granted = np.zeros(n, dtype=np.int64), np.zeros(n, dtype=np.int64)
+    asked = 0
+    for b in range(n):
+        qb = max(int(q[b]), 0)
+        c = int(ctx[b])
+        have, want = -(-c // page), -(-(c + qb) // page)
+        ok = c >= 0 and at + qb <= n_tok and want <= width
+        need = want - have if ok and free is not None else 0
+        asked += need
+        if need > 0 and asked > count:
+            ok = False
+        if ok:
+            for i in range(need):
+                table[b, have + i] = free[count - 1 - taken]
+                taken += 1
+            lens[b], granted[b] = c + qb, 1
+            for i in range(qb):
+                pos[at + i], seq[at + i] = c + i, b
+                slots[at + i] = table[b, (c + i) // page] * page + (c + i) % page
+        at += qb
+        cu.append(min(at, n_tok))
+    return np.array(cu), lens, pos, slots, seq, granted, count - taken
+
+
+def _plan_case(n, q_max, ctx_max, page, seed, pool=None, extra=0):
+    rng = np.random.Generator(np.random.PCG64(seed))
+    q = rng.integers(0, q_max + 1, n).astype(np.int32)
+    ctx = rng.integers(0, ctx_max + 1, n).astype(np.int32)
+    width = -(-(q_max + ctx_max) // page)
+    n_pages = n * width + 5
+    perm = rng.permutation(n_pages).astype(np.int32)
+    table = np.full((n, width), -1, dtype=np.int32)
+    o = 0
+    for b in range(n):
+        h = -(-int(ctx[b]) // page)
+        table[b, :h] = perm[o:o + h]
+        o += h
+    free = perm[o:]
+    count = len(free) if pool is None else min(pool, len(free))
+    return q, ctx, table, free, count, n_pages, int(q.sum()) + extra
+
+
+@pytest.mark.parametrize("n,q_max,ctx_max,page,pool,extra", [
+    (1, 1, 0, 16, None, 0), (1, 1, 100, 64, None, 3), (64, 1, 5000, 64, None, 0),
+    (5, 300, 40, 16, None, 70), (1000, 9, 200, 32, None, 11), (2500, 7, 60, 128, None, 0),
+    (8192, 2, 20, 16, None, 5), (3, 9000, 10, 16, None, 1), (40, 30, 100, 16, 37, 0),
+    (300, 40, 64, 16, 100, 9),
+])
+def test_plan_step(lib, n, q_max, ctx_max, page, pool, extra):
+    q, ctx, table, free, count, n_pages, n_tok = _plan_case(n, q_max, ctx_max, page, n + q_max, pool, extra)
+    ref_table = table.copy()
+    want = plan_reference(q, ctx, ref_table, page, n_tok, free, count)
+    d = lambda a: torch.as_tensor(np.ascontiguousarray(a), dtype=torch.int32, device="cuda")
+    tb, cnt, out = d(table), d([count]), d([-5])
+    got = lib.misa_plan_step(d(q), d(ctx), tb, page, n_tok=n_tok, n_pages=n_pages, free_pages=d(free),
+                             free_count=cnt, free_count_out=out)
+    st = lib.misa_last_device_status()
+    assert st == (lib.MISA_ERR_DEVICE if not want[5].all() else lib.MISA_OK)
+    for name, w in zip(("cu_q", "seq_lens", "positions", "slots", "seq_of", "granted"), want):
+        assert np.array_equal(getattr(got, name).cpu().numpy(), w), name
+    assert np.array_equal(tb.cpu().numpy(), ref_table)
+    assert int(out) == want[6] and int(cnt) == count
+    # in place: the lengths and the count are replaced
+    ln, tb2 = d(ctx), d(table)
+    lib.misa_plan_step(d(q), ln, tb2, page, n_tok=n_tok, n_pages=n_pages, free_pages=d(free),
+                       free_count=cnt, seq_lens=ln)
+    lib.misa_last_device_status()
+    assert np.array_equal(ln.cpu().numpy(), want[1]) and int(cnt) == want[6]
+    assert np.array_equal(tb2.cpu().numpy(), ref_table)
+    if pool is None:                              # complete tables: the maps alone
+        got = lib.misa_plan_step(d(q), d(ctx), tb, page, n_tok=n_tok, n_pages=n_pages)
+        assert lib.misa_last_device_status() == lib.MISA_OK
+        for name, w in zip(("cu_q", "seq_lens", "positions", "slots", "seq_of", "granted"), want):
+            assert np.array_equal(getattr(got, name).cpu().numpy(), w), name
+
+
+def test_plan_refuses_and_reports(lib):
+    d = lambda a: torch.as_tensor(a, dtype=torch.int32, device="cuda")
+    # too long for its table row; a negative length; rows that do not fit the buffers
+    q, ctx = d([2, 3, 4, 1, 5]), d([30, 15, -1, 0, 0])
+    tb = d([[1, 2]] * 5)
+    got = lib.misa_plan_step(q, ctx, tb, 16, n_tok=11, n_pages=10)
+    assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+    assert got.granted.tolist() == [1, 1, 0, 1, 0]
+    assert got.seq_lens.tolist() == [32, 18, 0, 1, 0]
+    assert got.cu_q.tolist() == [0, 2, 5, 9, 10, 11]
+    assert got.positions.tolist() == [30, 31, 15, 16, 17, -1, -1, -1, -1, 0, -1]
+    assert got.seq_of.tolist() == [0, 0, 1, 1, 1, -1, -1, -1, -1, 3, -1]
+    # a page id outside the pool: no slot
+    got = lib.misa_plan_step(d([1]), d([0]), d([[12]]), 16, n_tok=1, n_pages=10)
+    assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+    assert got.slots.tolist() == [-1] and got.positions.tolist() == [0]
+
+
+def test_release_gives_pages_back(lib):
+    d = lambda a: torch.as_tensor(a, dtype=torch.int32, device="cuda")
+    tb = d([[4, 5, 6], [7, 8, -1], [9, -1, -1], [1, 2, 3]])
+    lens, free, cnt = d([33, 32, 0, 48]), d([20, 21] + [0] * 10), d([2])
+    lib.misa_release_pages(d([1, 0, 1, 1]), lens, tb, 16, free, cnt)
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    assert int(cnt) == 8 and free.tolist()[:8] == [20, 21, 4, 5, 6, 1, 2, 3]
+    assert lens.tolist() == [0, 32, 0, 0]
+    lib.misa_release_pages(d([0, 1, 0, 0]), lens, tb, 16, free[:9].contiguous(), cnt)   # one too many
+    assert lib.misa_last_device_status() == lib.MISA_ERR_DEVICE
+    assert int(cnt) == 9
+
+
+def test_a_captured_step_advances_by_itself(lib):
+    # lengths, tables and the pool in place: each replay appends one token to each request
+    d = lambda a: torch.as_tensor(a, dtype=torch.int32, device="cuda")
+    n, page = 3, 16
+    q, lens = d([1, 1, 1]), d([0, 15, 40])
+    tb = d([[-1, -1, -1, -1], [30, -1, -1, -1], [31, 32, 33, -1]])
+    free, cnt = d(list(range(20))), d([20])
+    bufs = {k: torch.empty(n, dtype=torch.int32, device="cuda")
+            for k in ("positions", "slots", "seq_of", "granted")}
+    cu = torch.empty(n + 1, dtype=torch.int32, device="cuda")
+    args = dict(free_pages=free, free_count=cnt, seq_lens=lens, cu_q=cu, n_pages=64, **bufs)
+    lib.misa_plan_step(q, lens, tb, page, **args)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        lib.misa_plan_step(q, lens, tb, page, **args)
+    for i in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert lib.misa_last_device_status() == lib.MISA_OK
+    assert lens.tolist() == [21, 36, 61]
+    assert bufs["positions"].tolist() == [20, 35, 60]
+    assert tb.tolist() == [[19, 16, -1, -1], [30, 18, 15, -1], [31, 32, 33, 17]]
+    assert int(cnt) == 15
+    assert bufs["slots"].tolist() == [16 * 16 + 4, 15 * 16 + 3, 17 * 16 + 12]

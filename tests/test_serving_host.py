@@ -1,0 +1,178 @@
+"""Host-side checks of the serving operators (no GPU needed): refusals before any
+launch, the rotary frequencies, workspace sizes and the binding's size checks."""
+import ctypes
+import math
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from long_context_sparse_block_b200 import build
+    build.build()
+    from long_context_sparse_block_b200 import _lib
+    return _lib
+
+
+P = ctypes.c_void_p(16 * 1024)          # aligned, never dereferenced
+Q = ctypes.c_void_p(64 * 1024 * 1024)
+ODD = ctypes.c_void_p(16 * 1024 + 2)
+BIG = 1 << 40
+
+
+def _with(args, **changes):
+    out = dict(args)
+    out.update(changes)
+    return tuple(out.values())
+
+
+def _refusals(fn, good, inv, uns, cases):
+    for status, changes in cases:
+        assert fn(*_with(good, **changes)) == {"inv": inv, "uns": uns}.get(status, status), changes
+
+
+def test_plan_step_refusals(lib):
+    good = dict(q=P, c=P, n=4, bt=P, mb=8, ps=64, np=100, nt=16, fp=P, cap=10, fc=P, cu=P, sl=P,
+                pos=P, slot=P, so=P, gr=P, fo=P, s=None)
+    _refusals(lib._lib.misa_plan_step, good, lib.MISA_ERR_INVALID_ARG, lib.MISA_ERR_UNSUPPORTED, [
+        ("inv", dict(q=None)), ("inv", dict(c=ODD)), ("inv", dict(n=-1)), ("inv", dict(bt=None)),
+        ("inv", dict(mb=0)), ("uns", dict(ps=48)), ("uns", dict(ps=256)), ("inv", dict(np=0)),
+        ("inv", dict(np=1 << 25)), ("inv", dict(np=1 << 60)), ("inv", dict(nt=-1)),
+        ("inv", dict(cap=-1)), ("inv", dict(fc=None)), ("inv", dict(fo=None)), ("inv", dict(cu=None)),
+        ("inv", dict(sl=ODD)), ("inv", dict(pos=None)), ("inv", dict(slot=None)),
+        ("inv", dict(so=None)), ("inv", dict(gr=None)), ("uns", dict(n=8193)),
+    ])
+    rel = dict(r=P, sl=P, bt=P, n=4, mb=8, ps=64, np=100, fp=P, cap=10, fc=P, s=None)
+    _refusals(lib._lib.misa_release_pages, rel, lib.MISA_ERR_INVALID_ARG, lib.MISA_ERR_UNSUPPORTED, [
+        ("inv", dict(r=None)), ("inv", dict(fp=None)), ("inv", dict(fc=ODD)), ("uns", dict(ps=8)),
+        ("inv", dict(np=0)), ("inv", dict(cap=-1)), ("uns", dict(n=8193)), (0, dict(n=0)),
+    ])
+
+
+def test_rope_refusals(lib):
+    good = dict(x=P, pos=P, f=P, n=4, H=8, d=128, r=64, o=0, i=0, a=1.0, t=0, y=P, s=None)
+    cases = [
+        ("inv", dict(x=None)), ("inv", dict(x=ODD)), ("inv", dict(pos=None)), ("inv", dict(f=None)),
+        ("inv", dict(f=ctypes.c_void_p(16 * 1024 + 4))), ("inv", dict(n=-1)), ("inv", dict(H=0)),
+        ("uns", dict(d=96)), ("uns", dict(r=24)), ("uns", dict(o=4)), ("inv", dict(o=72)),
+        ("inv", dict(r=144)), ("inv", dict(i=2)), ("inv", dict(a=float("nan"))),
+        ("uns", dict(H=65536)), (0, dict(n=0)),
+    ]
+    inv, uns = lib.MISA_ERR_INVALID_ARG, lib.MISA_ERR_UNSUPPORTED
+    _refusals(lib._lib.misa_rope, good, inv, uns, cases + [("inv", dict(t=3)), ("inv", dict(y=ODD))])
+    f8 = dict(x=P, pos=P, f=P, n=4, H=8, d=128, r=64, o=0, i=0, a=1.0, y=P, ys=P, s=None)
+    _refusals(lib._lib.misa_rope_fp8, f8, inv, uns, cases + [("inv", dict(y=None)), ("inv", dict(ys=None))])
+    ap = dict(x=P, v=P, pos=P, sl=P, f=P, n=4, H=8, d=128, r=64, o=0, i=0, a=1.0, kd=0, kp=P, ks=None,
+              vp=P, ps=64, np=10, s=None)
+    _refusals(lib._lib.misa_cache_append, ap, inv, uns, cases + [
+        ("inv", dict(sl=None)), ("inv", dict(kp=ODD)), ("inv", dict(vp=None)), ("inv", dict(v=None)),
+        ("inv", dict(kd=1)), ("inv", dict(kd=2)), ("uns", dict(ps=20)), ("inv", dict(np=0)),
+        ("inv", dict(np=1 << 26)),
+    ])
+
+
+def test_attend_refusals(lib):
+    inv, uns = lib.MISA_ERR_INVALID_ARG, lib.MISA_ERR_UNSUPPORTED
+    shared = [
+        ("inv", dict(q=None)), ("inv", dict(q=ODD)), ("inv", dict(kp=None)), ("inv", dict(vp=ODD)),
+        ("inv", dict(bt=None)), ("inv", dict(mb=0)), ("uns", dict(ps=8)), ("inv", dict(np=0)),
+        ("inv", dict(np=1 << 60)), ("inv", dict(n=-1)), ("inv", dict(nt=-1)), ("inv", dict(H=0)),
+        ("inv", dict(Hk=3)), ("uns", dict(H=1032)), ("uns", dict(d=32)), ("uns", dict(d=96)),
+        ("inv", dict(sc=0.0)), ("inv", dict(sc=float("inf"))), ("inv", dict(sc=float("nan"))),
+        ("inv", dict(o=None)), ("inv", dict(l=ODD)), (0, dict(nt=0)), (0, dict(n=0)),
+        (lib.MISA_ERR_WORKSPACE, dict(ws=None)), (lib.MISA_ERR_WORKSPACE, dict(wb=1000)),
+        (lib.MISA_ERR_WORKSPACE, dict(ws=ODD)),
+    ]
+    good = dict(q=P, kp=P, vp=P, bt=P, mb=8, ps=64, np=100, cu=P, sl=P, n=2, nt=4, H=16, Hk=8, d=128,
+                sc=0.1, w=0, si=0, o=P, l=None, ws=P, wb=BIG, s=None)
+    _refusals(lib._lib.misa_attend_paged, good, inv, uns, shared + [
+        ("inv", dict(cu=None)), ("inv", dict(sl=None)), ("inv", dict(w=-1)), ("inv", dict(si=-1)),
+        ("inv", dict(si=4)),
+    ])
+    sel = dict(q=P, kp=P, vp=P, bt=P, mb=8, ps=64, np=100, so=P, pos=P, idx=P, k=64, n=2, nt=4, H=16,
+               Hk=8, d=128, sc=0.1, o=P, l=None, ws=P, wb=BIG, s=None)
+    _refusals(lib._lib.misa_attend_selected, sel, inv, uns, shared + [
+        ("inv", dict(so=None)), ("inv", dict(pos=None)), ("inv", dict(idx=None)), ("inv", dict(k=0)),
+        ("inv", dict(k=16385)),
+    ])
+
+
+def test_attend_workspace(lib):
+    ws = lambda d: lib.misa_workspace_size("attend", 1, 0, d, 0)
+    assert ws(128) > ws(64) > 0
+    assert ws(32) == 0 and ws(96) == 0
+
+
+def test_rope_frequencies(lib):
+    f, a = lib.misa_rope_frequencies(64, base=10000.0, device="cpu")
+    assert a == 1.0
+    for i in range(32):
+        assert math.isclose(float(f[i]), 10000.0 ** (-2 * i / 64), rel_tol=1e-14)
+    g, a = lib.misa_rope_frequencies(64, scaling="linear", factor=8.0, device="cpu")
+    assert a == 1.0
+    assert all(math.isclose(float(x) / 8, float(y), rel_tol=1e-15) for x, y in zip(f, g))
+    # base: the fastest pair kept, the slowest slowed by the factor
+    g, a = lib.misa_rope_frequencies(64, scaling="base", factor=8.0, device="cpu")
+    assert a == 1.0 and float(g[0]) == 1.0
+    assert math.isclose(float(f[31]) / float(g[31]), 8.0, rel_tol=1e-12)
+    # bands: fast pairs kept, slow ones divided, never outside the two, growing slower
+    g, a = lib.misa_rope_frequencies(64, scaling="bands", factor=40.0, trained_len=4096,
+                                     fast_turns=32, slow_turns=1, device="cpu")
+    assert math.isclose(a, 0.1 * math.log(40.0) + 1.0, rel_tol=1e-15)
+    for i in range(32):
+        turns = 4096 * float(f[i]) / (2 * math.pi)
+        ratio = float(f[i]) / float(g[i])
+        if turns >= 64:
+            assert ratio == 1.0
+        if turns <= 0.5:
+            assert math.isclose(ratio, 40.0, rel_tol=1e-12)
+        assert 1.0 <= ratio <= 40.0 * (1 + 1e-12)
+    same, a = lib.misa_rope_frequencies(64, scaling="bands", factor=1.0, device="cpu")
+    assert a == 1.0 and all(math.isclose(float(x), float(y), rel_tol=1e-14) for x, y in zip(f, same))
+
+
+def test_rope_frequencies_refusals(lib):
+    for kw in (dict(rope_dim=63), dict(rope_dim=0), dict(rope_dim=2048), dict(rope_dim=64, base=1.0),
+               dict(rope_dim=64, base=float("nan")), dict(rope_dim=64, scaling="linear", factor=0.5),
+               dict(rope_dim=64, scaling="linear", factor=float("inf")),
+               dict(rope_dim=64, scaling="bands", factor=2.0, trained_len=0.0),
+               dict(rope_dim=64, scaling="bands", factor=2.0, fast_turns=1.0, slow_turns=1.0),
+               dict(rope_dim=2, scaling="base", factor=2.0)):
+        with pytest.raises(lib.MisaError):
+            lib.misa_rope_frequencies(device="cpu", **kw)
+    with pytest.raises(ValueError):
+        lib.misa_rope_frequencies(64, scaling="other")
+
+
+def test_binding_checks_sizes_before_devices(lib):
+    import torch
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    f = torch.zeros(32, dtype=torch.float64)
+    pages = bf(10, 16, 2, 64)
+
+    def small(fn, *a, **kw):
+        with pytest.raises(ValueError, match="the call needs"):
+            fn(*a, **kw)
+
+    def host(fn, *a, **kw):
+        with pytest.raises(ValueError, match="must be a CUDA tensor"):
+            fn(*a, **kw)
+
+    host(lib.misa_plan_step, i32(4), i32(4), i32(4, 8), 16, n_tok=4)
+    small(lib.misa_plan_step, i32(3), i32(4), i32(4, 8), 16, n_tok=4)
+    small(lib.misa_release_pages, i32(3), i32(4), i32(4, 8), 16, i32(9), i32(1))
+    host(lib.misa_release_pages, i32(4), i32(4), i32(4, 8), 16, i32(9), i32(1))
+    host(lib.misa_rope, bf(4, 2, 64), i32(4), f)
+    host(lib.misa_rope_fp8, bf(4, 2, 64), i32(4), f)
+    host(lib.misa_cache_append, bf(4, 2, 64), i32(4), i32(4), f, pages)
+    small(lib.misa_cache_append, bf(4, 2, 64), i32(4), i32(4), f, pages, v=bf(4, 2, 32),
+          v_pages=bf(10, 16, 2, 64))
+    host(lib.misa_attend_paged, bf(4, 4, 64), pages, pages, i32(2, 8), i32(3), i32(2))
+    host(lib.misa_attend_selected, bf(4, 4, 64), pages, pages, i32(2, 8), i32(4), i32(4), i32(4, 9))
+    with pytest.raises(ValueError):               # shapes that do not go together
+        lib.misa_attend_paged(bf(4, 4, 128), pages, pages, i32(2, 8), i32(3), i32(2))
+    with pytest.raises(ValueError):
+        lib.misa_cache_append(bf(4, 3, 64), i32(4), i32(4), f, pages)
+    with pytest.raises(ValueError):
+        lib.misa_plan_step(i32(4), i32(4), i32(4, 8), 16)
