@@ -36,6 +36,7 @@
 // 1 MMA issuer, 3 scheduler, 2 query loader (and the zeroing of value rows past the end of
 // a sequence, which may hold anything, before the MMA reads them: 0 * NaN is
 // NaN), 4-7 and 8-11 the softmax of slots 0 and 1.
+#include <algorithm>
 #include <cstring>
 
 #include "internal.h"
@@ -60,7 +61,7 @@ struct AttLayout {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = OFF_Q + (LIST ? 1 : 2) * QTILE;
   static constexpr int OFF_BAR = OFF_KV + STAGES * TILE;
-  static constexpr int NBAR = 2 * STAGES + 14 + 2 * kSegs;
+  static constexpr int NBAR = 2 * STAGES + 16 + 2 * kSegs;
   static constexpr int OFF_SEG = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;
   static constexpr int OFF_ML = OFF_SEG + kSegs * 64;  // slot 1's (m, l) of 128 rows
   static constexpr int OFF_MISC = OFF_ML + 128 * 8;
@@ -92,6 +93,7 @@ struct AttParams {
   int H;
   int Hkv;
   int G;
+  int g_inv;                // 65536 / G + 1: x / G == x * g_inv >> 16 for x < 384, G <= 128
   int window;               // 0: none
   int sinks;
   int k;
@@ -198,7 +200,7 @@ struct __align__(16) Seg {
   int split;   // both slots share the rows (alternate tiles)
   int rows;    // valid rows of the unit
   int sink, lo;
-  int pad[2];
+  int tb, rem; // row m * 256 is query tb of the sequence, head rem of the group
   __device__ __forceinline__ int key0(int i) const { return (i < sink ? i : lo + i - sink) * kTile; }
   // tiles of a slot
   __device__ __forceinline__ int tiles_of(int slot) const {
@@ -251,7 +253,7 @@ struct Walk {
         g.p0 = __ldg(p.positions + g.m);
         g.len = 0;
         g.rows = p.G;
-        g.sink = g.lo = 0;
+        g.sink = g.lo = g.tb = g.rem = 0;
         g.split = 1;
         g.part = g.i0 > 0 ? 2 * cta : g.i1 < nt ? 2 * cta + 1 : -1;
         g.valid = 1;
@@ -287,6 +289,9 @@ struct Walk {
         g.rows = t.rows;
         g.sink = t.sink;
         g.lo = t.lo;
+        const int64_t r0 = static_cast<int64_t>(g.m) * kBlockRows;
+        g.tb = static_cast<int>(r0 / p.G);
+        g.rem = static_cast<int>(r0 % p.G);
         g.split = t.rows <= kTile;
         g.part = g.i0 > 0 ? 2 * cta : g.i1 < t.n ? 2 * cta + 1 : -1;
         g.valid = 1;
@@ -440,6 +445,13 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
 // The low n bits (n clamped to 0..32).
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -491,20 +503,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, ctl));
 }
 
-// Places of a segment's tiles in the ring: K_0, K_1, V_0, K_2, V_1, .., V_{n-1}.
-__device__ __forceinline__ uint32_t k_at(int x) { return x == 0 ? 0u : 2u * x - 1u; }
-__device__ __forceinline__ uint32_t v_at(int x, int n) { return x == n - 1 ? 2u * n - 1u : 2u * x + 2u; }
-
-// Unnormalised O of a TMEM row, 32 columns at a time, to f(column, values).
-template <int D, typename F>
-__device__ __forceinline__ void for_o(uint32_t taddr, F&& f) {
-#pragma unroll
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    uint32_t v[32];
-    tmem_ld32(taddr + c0, v);
-    tmem_wait_ld_regs(v);
-    f(c0, v);
-  }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 template <int D, bool LIST>
@@ -521,7 +528,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   constexpr int FULL = 0, EMPTY = ST, QFULL = 2 * ST, QEMPTY = QFULL + 1, SFULL = QFULL + 2,
-                PFULL = SFULL + 2, OFULL = PFULL + 2, OEMPTY = OFULL + 2, MLFULL = OEMPTY + 2,
+                PFULL = SFULL + 2, OFULL = PFULL + 4, OEMPTY = OFULL + 2, MLFULL = OEMPTY + 2,
                 MLEMPTY = MLFULL + 1, VREADY = MLEMPTY + 1, VTAIL = VREADY + 1, GFULL = VTAIL + 1,
                 GEMPTY = GFULL + kSegs;
   static_assert(GEMPTY + kSegs == L::NBAR, "barriers");
@@ -560,7 +567,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     mbar_init(bar(QEMPTY), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(SFULL + i), 1);
-      mbar_init(bar(PFULL + i), 4);
+      mbar_init(bar(PFULL + 2 * i), 4);
+      mbar_init(bar(PFULL + 2 * i + 1), 4);
       mbar_init(bar(OFULL + i), 1);
       mbar_init(bar(OEMPTY + i), 4);
     }
@@ -602,7 +610,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   if (warp == 0) {
     if constexpr (!LIST) {
       // -------------------------------------------------------- key / value loader
-      uint32_t ring = 0;
+      int stage = 0;
+      uint32_t phase = 0;
       bool ok = true;
       const int page = 1 << p.page_shift, per = kTile / page;
       for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
@@ -625,8 +634,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
           return static_cast<int>(y);
         };
-        auto load = [&](const CUtensorMap* map, uint32_t at, int y) -> bool {
-          const uint32_t e = ring + at, stage = e % ST, phase = (e / ST) & 1;
+        auto load = [&](const CUtensorMap* map, int y) -> bool {
           if (!warp_wait(bar(EMPTY + stage), phase ^ 1, abort_flag, p.ctl)) return false;
           if (lane == 0) mbar_arrive_expect_tx(bar(FULL + stage), L::TILE);
           __syncwarp();
@@ -636,106 +644,167 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               tma_load_3d(sKV + stage * L::TILE + c * L::CHUNK + lane * page * 128, map,
                           bar(FULL + stage), c * 64, g.j, y);
           }
+          if (++stage == ST) {
+            stage = 0;
+            phase ^= 1;
+          }
           return true;
         };
         int y_cur = page_row(0), y_next = page_row(1), y_prev = 0;
-        for (int x = 0; x <= n && ok; ++x) {
-          if (x < n) ok = load(&kmap, k_at(x), y_cur);
-          if (ok && x > 0) ok = load(&vmap, v_at(x - 1, n), y_prev);
+        // the order in which the MMA warp takes them (see there)
+        for (int x = 0; x < n + g.split && ok; ++x) {
+          if (x < n) ok = load(&kmap, y_cur);
+          if (!g.split)
+            ok = ok && load(&vmap, y_cur);
+          else if (ok && x > 0)
+            ok = load(&vmap, y_prev);
           y_prev = y_cur;
           y_cur = y_next;
           y_next = page_row(x + 2);
         }
         if (!ok) break;
-        ring += 2 * n;
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      uint32_t ring = 0, tails = 0;
-      uint32_t used[2] = {0, 0};   // segments in which the slot had tiles
-      uint32_t pcount[2] = {0, 0}; // tiles of the slot so far
-      bool ok = true;
-      constexpr uint32_t id_qk = umma_idesc_bf16_f32(kTile, kTile);
-      constexpr uint32_t id_pv = umma_idesc_bf16_f32(kTile, D) | (1u << 16);  // B is MN-major
-      for (; seg_wait(sg); ++sg) {
-        const Seg g = seg_at(sg);
-        seg_done(sg);
-        const int n = g.i1 - g.i0;
-        const int n0 = g.tiles_of(0), n1 = g.tiles_of(1);
-        int qk_left = n0 + n1;
-        const bool tail = !LIST && g.len > g.key0(g.i1 - 1) && g.len < g.key0(g.i1 - 1) + kTile;
-        ok = mbar_wait(bar(QFULL), sg & 1, abort_flag, p.ctl);
-        if (!ok) break;
-        fence_proxy_async_smem();  // the query rows' copies -> MMA operand reads
-        bool told = !tail;
-        auto full = [&](uint32_t at, uint32_t& stage) -> bool {
-          const uint32_t e = ring + at;
-          stage = e % ST;
-          if (!mbar_wait(bar(FULL + stage), (e / ST) & 1, abort_flag, p.ctl)) return false;
-          // entries up to at - 2 have been waited for, so from here on the last
-          // tile's values are the next to fill their stage: its phase can be
-          // waited for by parity
-          if (!told && at + ST >= 2u * n + 1u) {
-            mbar_arrive(bar(VTAIL));
-            told = true;
-          }
-          if (LIST) fence_proxy_async_smem();
-          tc_fence_after();
-          return true;
-        };
-        auto qk = [&](int slot, int i) -> bool {  // S of the slot's i-th tile
-          const int x = g.split ? 2 * i + slot : i;
-          uint32_t stage;
-          if (!full(k_at(x), stage)) return false;
-          const uint32_t a = sQ + (g.split ? 0 : slot) * L::QTILE, b = sKV + stage * L::TILE;
+    // The whole warp runs the control flow, so that descriptors and addresses
+    // stay warp-uniform; one elected lane issues.  (With everything under
+    // `lane == 0` the issue of a step took 4200 cycles instead of 2048 of
+    // tensor work.)
+    const bool leader = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, tails = 0;
+    uint32_t used[2] = {0, 0};   // segments in which the slot had tiles
+    uint32_t pcount[2] = {0, 0}; // tiles of the slot so far
+    bool ok = true;
+    constexpr uint32_t id_qk = umma_idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t id_pv = umma_idesc_bf16_f32(kTile, D) | (1u << 16);  // B is MN-major
+    const uint64_t dq = umma_desc_kmajor(sQ, 128), dk = umma_desc_kmajor(sKV, 128),
+                   dv = umma_desc_mnmajor(sKV, L::CHUNK);
+    auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.ctl); };
+    auto commit = [&](int i) {
+      if (leader) tc_commit(bar(i));
+    };
+    for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
+      const Seg& gs = seg_at(sg);
+      const int n = __shfl_sync(0xffffffffu, gs.i1 - gs.i0, 0);
+      const bool split = __shfl_sync(0xffffffffu, gs.split, 0) != 0;
+      const int key0 = gs.key0(gs.i1 - 1);
+      const bool tail =
+          __shfl_sync(0xffffffffu, !LIST && gs.len > key0 && gs.len < key0 + kTile, 0) != 0;
+      __syncwarp();
+      if (lane == 0) seg_done(sg);
+      bool told = !tail;
+      int at = 0;  // ring entries of this segment waited for
+      // The next ring entry's stage, once its tile is there.
+      auto next = [&](int& st) -> bool {
+        if (!wait(FULL + stage, phase)) return false;
+        st = stage;
+        if (++stage == ST) {
+          stage = 0;
+          phase ^= 1;
+        }
+        ++at;
+        // the entry that the last tile's values replace has been seen: their
+        // phase can be waited for by parity
+        if (!told && at + ST >= 2 * n) {
+          if (lane == 0) mbar_arrive(bar(VTAIL));
+          told = true;
+        }
+        if (LIST) fence_proxy_async_smem();
+        tc_fence_after();
+        return true;
+      };
+      auto qk = [&](int slot, int st) {  // S of the slot
+        const uint64_t a = dq + (split ? 0 : slot) * (L::QTILE >> 4);
+        const uint64_t b = dk + st * (L::TILE >> 4);
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = (kk / 4) * L::CHUNK + (kk % 4) * 32;
-            tc_mma_bf16(tmem_base + slot * kTile, umma_desc_kmajor(a + o, 128),
-                        umma_desc_kmajor(b + o, 128), id_qk, kk > 0 ? 1u : 0u);
+            const uint32_t o = ((kk / 4) * L::CHUNK + (kk % 4) * 32) >> 4;
+            tc_mma_bf16(tmem_base + slot * kTile, a + o, b + o, id_qk, kk > 0 ? 1u : 0u);
           }
-          if (g.split || slot == 1) tc_commit(bar(EMPTY + stage));
-          tc_commit(bar(SFULL + slot));
-          if (--qk_left == 0) tc_commit(bar(QEMPTY));  // the query rows are free again
-          return true;
-        };
-        auto pv = [&](int slot, int i) -> bool {  // O += P V of the slot's i-th tile
-          const int x = g.split ? 2 * i + slot : i;
-          uint32_t stage;
-          if (!full(v_at(x, n), stage)) return false;
-          if (tail && x == n - 1 && (g.split || slot == 0)) {
-            if (!mbar_wait(bar(VREADY), tails & 1, abort_flag, p.ctl)) return false;
-            fence_proxy_async_smem();
-          }
-          if (i == 0 &&
-              !mbar_wait(bar(OEMPTY + slot), (used[slot] & 1) ^ 1, abort_flag, p.ctl))
-            return false;
-          if (!mbar_wait(bar(PFULL + slot), pcount[slot] & 1, abort_flag, p.ctl)) return false;
-          tc_fence_after();
-          const uint32_t b = sKV + stage * L::TILE;
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_bf16_ta(tmem_base + 256 + slot * D, tmem_base + slot * kTile + kk * 8,
-                           umma_desc_mnmajor(b + kk * 2048, L::CHUNK), id_pv,
-                           i > 0 || kk > 0 ? 1u : 0u);
-          ++pcount[slot];
-          if (g.split || slot == 1) tc_commit(bar(EMPTY + stage));
-          if (i == g.tiles_of(slot) - 1) tc_commit(bar(OFULL + slot));
-          return true;
-        };
-        ok = qk(0, 0) && (n1 == 0 || qk(1, 0));
-        for (int i = 0; ok && i < n0; ++i) {
-          ok = pv(0, i) && (i + 1 >= n0 || qk(0, i + 1));
-          if (ok && i < n1) ok = pv(1, i) && (i + 1 >= n1 || qk(1, i + 1));
         }
-        if (!ok) break;
-        ring += 2 * n;
+      };
+      auto pv = [&](int slot, int st, bool first) -> bool {  // O += P V of the slot
+        const uint64_t b = dv + st * (L::TILE >> 4);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // the first half of P is there early
+          if (!wait(PFULL + 2 * slot + half, pcount[slot] & 1)) return false;
+          tc_fence_after();
+          if (leader) {
+#pragma unroll
+            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+              tc_mma_bf16_ta(tmem_base + 256 + slot * D, tmem_base + slot * kTile + kk * 8,
+                             b + kk * (2048 >> 4), id_pv, kk > 0 || !first ? 1u : 0u);
+          }
+        }
+        ++pcount[slot];
+        return true;
+      };
+      auto tail_ready = [&]() -> bool {  // rows past the sequence have been zeroed
+        if (!wait(VREADY, tails & 1)) return false;
+        fence_proxy_async_smem();
+        ++tails;
+        return true;
+      };
+      ok = wait(QFULL, sg & 1);
+      if (!ok) break;
+      fence_proxy_async_smem();  // the query rows' copies -> MMA operand reads
+      if (split) {
+        for (int x = -2; x < n && ok; ++x) {
+          const int slot = x & 1;
+          int st;
+          if (x >= 0) {
+            ok = next(st) && (x < n - 1 || !tail || tail_ready()) &&
+                 (x > 1 || wait(OEMPTY + slot, (used[slot] & 1) ^ 1)) && pv(slot, st, x < 2);
+            if (!ok) break;
+            commit(EMPTY + st);
+            if (x + 2 >= n) commit(OFULL + slot);
+          }
+          if (x + 2 < n) {
+            ok = next(st);
+            if (!ok) break;
+            qk(slot, st);
+            commit(EMPTY + st);
+            commit(SFULL + slot);
+            if (x + 3 == n) commit(QEMPTY);  // the query rows are free again
+          }
+        }
         ++used[0];
-        if (n1 > 0) ++used[1];
-        if (tail) ++tails;
+        if (n > 1) ++used[1];
+      } else {
+        int sk = 0, sv;
+        for (int i = -1; i < n && ok; ++i) {
+          if (i >= 0) {
+            ok = next(sv) && (i < n - 1 || !tail || tail_ready()) &&
+                 (i > 0 || wait(OEMPTY, (used[0] & 1) ^ 1)) && pv(0, sv, i == 0);
+            if (!ok) break;
+            if (i == n - 1) commit(OFULL);
+          }
+          if (i + 1 < n) {
+            ok = next(sk);
+            if (!ok) break;
+            qk(0, sk);
+            commit(SFULL);
+          }
+          if (i >= 0) {
+            ok = (i > 0 || wait(OEMPTY + 1, (used[1] & 1) ^ 1)) && pv(1, sv, i == 0);
+            if (!ok) break;
+            commit(EMPTY + sv);
+            if (i == n - 1) commit(OFULL + 1);
+          }
+          if (i + 1 < n) {
+            qk(1, sk);
+            commit(EMPTY + sk);
+            commit(SFULL + 1);
+            if (i + 2 == n) commit(QEMPTY);
+          }
+        }
+        ++used[0];
+        ++used[1];
       }
+      if (!ok) break;
     }
     __syncwarp();
   } else if (warp == 3) {
@@ -763,24 +832,21 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (lane == 0) seg_done(sg);
       const int n = g.i1 - g.i0;
       if (!warp_wait(bar(QEMPTY), (sg & 1) ^ 1, abort_flag, p.ctl)) break;
+      // only the rows that exist: what the others hold stays in their own rows of S
       constexpr int UPR = D / 8;
-      const int tile_rows = g.split ? kTile : kBlockRows;
-      const int64_t r0 = LIST ? 0 : static_cast<int64_t>(g.m) * kBlockRows;
+      const int u = lane % UPR;
+      const uint16_t* src = p.Q + (static_cast<int64_t>(g.t0 + g.tb) * p.H + g.j * p.G) * D + u * 8;
 #pragma unroll 4
-      for (int x = lane; x < tile_rows * UPR; x += 32) {
-        const int r = x / UPR, u = x % UPR;
-        const bool in = r < g.rows;
-        const int64_t rr = r0 + (in ? r : 0);
-        const int64_t t = g.t0 + rr / p.G;
-        const int h = g.j * p.G + static_cast<int>(rr % p.G);
+      for (int r = lane / UPR; r < g.rows; r += 32 / UPR) {
+        const int x = r + g.rem, q = x * p.g_inv >> 16;
         cp_async16(sQ + (r / kTile) * L::QTILE + (u / 8) * L::CHUNK + swz_offset(r % kTile, u % 8, 128),
-                   p.Q + (t * p.H + h) * D + u * 8, in ? 16u : 0u);
+                   src + (static_cast<int64_t>(q) * p.H + (x - q * p.G)) * D, 16u);
       }
       cp_async_mbar_arrive_noinc(bar(QFULL));
       const int key0 = g.key0(g.i1 - 1);
       if (!LIST && g.len > key0 && g.len < key0 + kTile) {
         // the last tile's value rows past the end of the sequence
-        const uint32_t e = ring + v_at(n - 1, n), stage = e % ST;
+        const uint32_t e = ring + 2 * n - 1, stage = e % ST;  // the segment's last entry
         ok = warp_wait(bar(VTAIL), tails & 1, abort_flag, p.ctl) &&
              warp_wait(bar(FULL + stage), (e / ST) & 1, abort_flag, p.ctl);
         if (!ok) break;
@@ -823,7 +889,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if constexpr (LIST) {
         pos = g.p0;
       } else {
-        pos = live ? g.p0 + static_cast<int>((static_cast<int64_t>(g.m) * kBlockRows + r) / p.G) : -1;
+        pos = live ? g.p0 + g.tb + ((r + g.rem) * p.g_inv >> 16) : -1;
       }
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < n; ++i) {
@@ -867,9 +933,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int q = 0; q < 128; q += 4)
+          for (int q = 0; q < 32; q += 2)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) mx[y] = fmaxf(mx[y], __uint_as_float(v[(q + y) >> 5][(q + y) & 31]));
+            for (int y = 0; y < 4; ++y)
+              mx[y] = fmaxf(fmaxf(mx[y], __uint_as_float(v[y][q])), __uint_as_float(v[y][q + 1]));
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
           if (__any_sync(0xffffffffu, top > m + (i == 0 ? 0.0f : kRaise))) {
             const bool raise = top > m + (i == 0 ? 0.0f : kRaise);
@@ -891,7 +958,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             m = mn;
           }
           const float ref = m == -INFINITY ? 0.0f : m;
-          float2 sum = make_float2(0.0f, 0.0f);
           const float2 cc = make_float2(p.c, p.c), nr = make_float2(-ref, -ref);
 #pragma unroll
           for (int q0 = 0; q0 < 4; ++q0) {
@@ -901,26 +967,41 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
               const float2 z = fma2(make_float2(__uint_as_float(v[q0][2 * q]),
                                                 __uint_as_float(v[q0][2 * q + 1])), cc, nr);
               const float e0 = ex2(z.x), e1 = ex2(z.y);
-              sum.x += e0;
-              sum.y += e1;
+              v[q0][2 * q] = __float_as_uint(e0);
+              v[q0][2 * q + 1] = __float_as_uint(e1);
               o[q] = bf16x2(e0, e1);
             }
             tmem_st16(tS + q0 * 16, o);
+            if (q0 & 1) {  // half of P is there: its products can start
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar(PFULL + 2 * slot + (q0 >> 1)));
+            }
           }
-          l += sum.x + sum.y;
-          tmem_wait_st();
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+          for (int q = 0; q < 128; q += 4)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              sum[y] = add2(sum[y], make_float2(__uint_as_float(v[q >> 5][(q & 31) + 2 * y]),
+                                                __uint_as_float(v[q >> 5][(q & 31) + 2 * y + 1])));
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(PFULL + 2 * slot));
+            mbar_arrive(bar(PFULL + 2 * slot + 1));
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(PFULL + slot));
       }
       if (!ok) break;
 
       // ---- the segment's result
-      const int64_t rr = (LIST ? 0 : static_cast<int64_t>(g.m) * kBlockRows) + r;
-      const int64_t t = g.t0 + rr / p.G;
-      const int h = g.j * p.G + static_cast<int>(rr % p.G);
-      const int64_t orow = t * p.H + h;
+      const int rq = (r + g.rem) * p.g_inv >> 16;
+      const int64_t orow =
+          static_cast<int64_t>(g.t0 + g.tb + rq) * p.H + g.j * p.G + (r + g.rem - rq * p.G);
       if (g.split && slot == 1) {
         // (m, l) to slot 0, which joins the two halves of the tiles
         ok = warp_wait(bar(MLEMPTY), (segs_split & 1) ^ 1, abort_flag, p.ctl);
@@ -1010,7 +1091,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       // -------------------------------------------------------- row loader of the list form
       reg_dec<64>();
       const int r = threadIdx.x - 384;  // entry of the tile
-      uint32_t ring = 0;
+      int stage = 0;
+      uint32_t phase = 0;
       bool ok = true;
       const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
       for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
@@ -1024,44 +1106,60 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           const int64_t e = static_cast<int64_t>(g.i0 + x) * kTile + r;
           return x < n && e < p.k ? __ldg(list + e) : -1;
         };
-        auto phys = [&](int s) -> int64_t {  // cache row of token s, or -1: not visible
+        // The table entry of token s, and from it the cache row (-1: not visible).
+        // Tokens are read three tiles ahead and entries two, so neither latency
+        // stands between two tiles' copies.
+        auto entry_page = [&](int s) -> int {
+          return s >= 0 && s <= g.p0 && s < cap ? __ldg(bt + (s >> p.page_shift)) : 0;
+        };
+        auto phys = [&](int s, int pg) -> int {
           if (s < 0 || s > g.p0) return -1;
           if (s >= cap) {
             report(p.ctl, DEV_BAD_INPUT);
             return -1;
           }
-          int64_t pg = __ldg(bt + (s >> p.page_shift));
           if (pg < 0 || pg >= p.n_pages) {
             report(p.ctl, DEV_BAD_INPUT);
             pg = 0;
           }
           return (pg << p.page_shift) | (s & ((1 << p.page_shift) - 1));
         };
-        auto load = [&](const uint16_t* pool, uint32_t at, int64_t y) -> bool {
-          const uint32_t e = ring + at, stage = e % ST, phase = (e / ST) & 1;
+        auto load = [&](const uint16_t* pool, int y) -> bool {
           if (!warp_wait(bar(EMPTY + stage), phase ^ 1, abort_flag, p.ctl)) return false;
-          const uint16_t* src = pool + ((y < 0 ? 0 : y) * p.Hkv + g.j) * D;
-          const uint32_t dst = sKV + stage * L::TILE;
+          // the lanes of a row's units side by side: whole 128-byte lines per
+          // instruction (a thread per row fetched every 32-byte sector twice)
+          constexpr int UPR = D / 8;
+          const int u = lane % UPR;
+          const uint16_t* base = pool + g.j * D + u * 8;
+          const uint32_t dst = sKV + stage * L::TILE + (u / 8) * L::CHUNK;
 #pragma unroll
-          for (int u = 0; u < D / 8; ++u)
-            cp_async16(dst + (u / 8) * L::CHUNK + swz_offset(r, u % 8, 128), src + u * 8,
-                       y < 0 ? 0u : 16u);
+          for (int i = 0; i < UPR; ++i) {
+            const int rl = i * (32 / UPR) + lane / UPR;
+            const int yr = __shfl_sync(0xffffffffu, y, rl);
+            cp_async16(dst + swz_offset((r & ~31) + rl, u % 8, 128),
+                       base + static_cast<int64_t>(yr < 0 ? 0 : yr) * p.Hkv * D, yr < 0 ? 0u : 16u);
+          }
           cp_async_mbar_arrive_noinc(bar(FULL + stage));
+          if (++stage == ST) {
+            stage = 0;
+            phase ^= 1;
+          }
           return true;
         };
-        int s_next = entry(1);
-        int64_t y_cur = phys(entry(0)), y_prev = -1;
+        int s0 = entry(0), s1 = entry(1), s2 = entry(2);
+        int pg0 = entry_page(s0), pg1 = entry_page(s1);
+        int y = phys(s0, pg0), y_prev = -1;
         for (int x = 0; x <= n && ok; ++x) {
-          const int s_after = entry(x + 2);
-          if (x < n) ok = load(p.kp, k_at(x), y_cur);
-          const int64_t y_next = phys(s_next);
-          if (ok && x > 0) ok = load(p.vp, v_at(x - 1, n), y_prev);
-          y_prev = y_cur;
-          y_cur = y_next;
-          s_next = s_after;
+          const int s3 = entry(x + 3), pg2 = entry_page(s2);
+          if (x < n) ok = load(p.kp, y);
+          if (ok && x > 0) ok = load(p.vp, y_prev);
+          y_prev = y;
+          y = phys(s1, pg1);
+          s1 = s2;
+          pg1 = pg2;
+          s2 = s3;
         }
         if (!ok) break;
-        ring += 2 * n;
       }
       cp_async_wait_all();
     }
@@ -1077,10 +1175,16 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
 }
 
 // Joins the parts of the unit that CTA blockIdx.x opened and did not finish:
-// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, parts in CTA order.  Each
-// warp takes a row at a time.
+// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, parts in CTA order.  A warp
+// takes a row: its lanes hold the parts' m and l, 32 at a time.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 8;      // blocks in y, 8 rows each at a time
+constexpr int kMaxCtas = 256;
+
 template <int D, bool LIST>
-__global__ void __launch_bounds__(256) join_kernel(const AttParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttParams p, int ctas) {
+  __shared__ int parts[kMaxCtas];  // workspace slots of the unit's parts, in order
+  __shared__ int first_end, warp_n[kJoinThreads / 32];
   const int c = blockIdx.x;
   const int4 open = p.head[2 * c + 1];
   if (!open.x) return;
@@ -1098,47 +1202,88 @@ __global__ void __launch_bounds__(256) join_kernel(const AttParams p, int ctas) 
     t0 = s.t0;
     rows = t.rows;
   }
+  if (static_cast<int>(blockIdx.y) * 8 >= rows) return;
   // the CTAs that follow, up to the one that ends the unit (a CTA whose share
   // of it is less than a tile has no part)
-  int last = c;
-  for (int e = c + 1; e < ctas; ++e) {
-    const int4 cont = p.head[2 * e];
-    if (cont.x) last = e;
-    if (cont.y) break;
+  const int e = c + 1 + static_cast<int>(threadIdx.x);
+  const int4 cont = e < ctas ? p.head[2 * e] : make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0) first_end = ctas;
+  __syncthreads();
+  if (cont.y) atomicMin(&first_end, e);
+  __syncthreads();
+  const bool mine = cont.x && e <= first_end;
+  const uint32_t vote = __ballot_sync(0xffffffffu, mine);
+  if (lane_id() == 0) warp_n[warp_id()] = __popc(vote);
+  __syncthreads();
+  int at = 1, n = 1;
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    if (w < warp_id()) at += warp_n[w];
+    n += warp_n[w];
   }
+  if (mine) parts[at + __popc(vote & ((1u << lane_id()) - 1u))] = 2 * e;
+  if (threadIdx.x == 0) parts[0] = 2 * c + 1;
+  __syncthreads();
+
+  constexpr int V = D / 32;  // elements of a lane
   const int lane = lane_id();
   for (int r = blockIdx.y * 8 + warp_id(); r < rows; r += gridDim.y * 8) {
-    float m = -INFINITY;
-    for (int e = c; e <= last; ++e) {
-      if (e > c && !p.head[2 * e].x) continue;
-      const int64_t q = static_cast<int64_t>(e == c ? 2 * e + 1 : 2 * e) * kBlockRows + r;
-      m = fmaxf(m, p.ml[2 * q]);
-    }
-    const float ref = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[D / 32];
+    float m = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
-    for (int e = c; e <= last; ++e) {
-      if (e > c && !p.head[2 * e].x) continue;
-      const int64_t q = static_cast<int64_t>(e == c ? 2 * e + 1 : 2 * e) * kBlockRows + r;
-      const float f = ex2(p.ml[2 * q] - ref);
-      l = fmaf(f, p.ml[2 * q + 1], l);
+    for (int i = 0; i < V; ++i) o[i] = 0.0f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      float pm = -INFINITY, pl = 0.0f;
+      int64_t q = 0;
+      if (i0 + lane < n) {
+        q = static_cast<int64_t>(parts[i0 + lane]) * kBlockRows + r;
+        const float2 x = *reinterpret_cast<const float2*>(p.ml + 2 * q);
+        pm = x.x;
+        pl = x.y;
+      }
+      float top = fmaxf(pm, m);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) o[i] = fmaf(f, p.po[q * D + i * 32 + lane], o[i]);
+      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float f0 = ex2(m - ref), f = ex2(pm - ref);
+      float lsum = f * pl;
+#pragma unroll
+      for (int s = 16; s > 0; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
+      l = l * f0 + lsum;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] *= f0;
+      m = top;
+      const int left = min(32, n - i0);
+#pragma unroll 4
+      for (int x = 0; x < left; ++x) {
+        const float w = __shfl_sync(0xffffffffu, f, x);
+        const int64_t qx = __shfl_sync(0xffffffffu, q, x);
+        float y[V];
+        if constexpr (V == 4) {
+          const float4 z = *reinterpret_cast<const float4*>(p.po + qx * D + lane * V);
+          y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
+        } else {
+          const float2 z = *reinterpret_cast<const float2*>(p.po + qx * D + lane * V);
+          y[0] = z.x, y[1] = z.y;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] = fmaf(w, y[i], o[i]);
+      }
     }
     const int64_t rr = (LIST ? 0 : static_cast<int64_t>(open.z) * kBlockRows) + r;
     const int64_t row = (t0 + rr / p.G) * p.H + open.w * p.G + rr % p.G;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    uint32_t w[V / 2];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
-      p.out[row * D + i * 32 + lane] =
-          static_cast<uint16_t>(bf16x2(o[i] * inv, 0.0f) & 0xffffu);
+    for (int i = 0; i < V / 2; ++i) w[i] = bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(p.out + row * D + lane * V) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V) = w[0];
     if (p.lse && lane == 0)
       p.lse[row] = l > 0.0f ? (m + __log2f(l)) * 0.69314718055994530942f : l == 0.0f ? -INFINITY : l;
   }
 }
 
-int att_ctas() { return sm_count(); }
+int att_ctas() { return std::min(sm_count(), kMaxCtas); }
 
 struct AttWs {
   size_t head, ml, po, total;
@@ -1166,7 +1311,7 @@ cudaError_t launch_att(const AttParams& p, const CUtensorMap& km, const CUtensor
   kern<<<n, L::THREADS, L::ALLOC, s>>>(km, vm, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  join_kernel<D, LIST><<<dim3(n, 4), 256, 0, s>>>(p, n);
+  join_kernel<D, LIST><<<dim3(n, kJoinRows), kJoinThreads, 0, s>>>(p, n);
   return cudaGetLastError();
 }
 
@@ -1196,6 +1341,7 @@ cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t
   p.H = a.H;
   p.Hkv = a.Hkv;
   p.G = a.H / a.Hkv;
+  p.g_inv = 65536 / p.G + 1;
   p.window = a.window;
   p.sinks = a.sinks;
   p.k = a.k;
