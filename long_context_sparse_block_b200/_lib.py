@@ -549,7 +549,7 @@ def _raw_stream(dev: int) -> int:
     if torch.cuda.current_device() != dev:
         raise ValueError(f"the tensors are on cuda:{dev}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)  # (current_stream() builds an object each time)
 
 
 class StepPlan(NamedTuple):
@@ -736,7 +736,7 @@ def _attend_args(Q, k_pages, v_pages, block_tables, scale, out, want_lse, lse, w
     if out is None:
         out = torch.empty_like(Q)
     if lse is None and want_lse:
-        lse = torch.empty((n_tok, H), dtype=torch.float32, device=Q.device)
+        lse = Q.new_empty((n_tok, H), dtype=torch.float32)
     pages = (_arg(Q, 0, _BF16_CODES, "Q", dev), _arg(k_pages, 0, _BF16_CODES, "k_pages", dev),
              _arg(v_pages, 0, _BF16_CODES, "v_pages", dev),
              _arg(block_tables, 0, _I32, "block_tables", dev), max_blocks, page_size, n_pages)

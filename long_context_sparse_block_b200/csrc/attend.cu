@@ -36,19 +36,16 @@
 // 1 MMA issuer, 3 scheduler, 2 query loader (and the zeroing of value rows past the end of
 // a sequence, which may hold anything, before the MMA reads them: 0 * NaN is
 // NaN), 4-7 and 8-11 the softmax of slots 0 and 1.
-#include <algorithm>
+#include <atomic>
 #include <cstring>
 
-#include "internal.h"
+#include "attend.cuh"
 
 namespace misa {
 namespace {
 
-constexpr int kTile = 128;       // keys per tile
-constexpr int kBlockRows = 256;  // rows of a unit (two slots of 128)
 constexpr int kSegs = 4;         // segments published ahead
 constexpr uint64_t kDrainNs = 2000000;
-constexpr float kRaise = 8.0f;   // log2 of the largest weight before m is raised
 
 template <int D, bool LIST>
 struct AttLayout {
@@ -71,121 +68,6 @@ struct AttLayout {
   static constexpr int ALLOC = BYTES + 1024;
   static_assert(ALLOC <= 232448, "shared memory of an SM");
 };
-
-struct AttParams {
-  const uint16_t* Q;        // [n_tok, H, D]
-  const uint16_t* kp;       // [n_pages, page, Hkv, D]
-  const uint16_t* vp;
-  const int32_t* bts;       // [n_seq, max_blocks]
-  const int32_t* cu_q;      // [n_seq + 1]
-  const int32_t* lens;      // [n_seq]
-  const int32_t* seq_of;    // list form: [n_tok]
-  const int32_t* positions; // list form: [n_tok]
-  const int32_t* idx;       // list form: [n_tok, k]
-  uint16_t* out;            // [n_tok, H, D]
-  float* lse;               // [n_tok, H], nullable
-  int64_t n_pages;
-  int64_t key_rows;
-  int max_blocks;
-  int page_shift;
-  int n_seq;
-  int n_tok;
-  int H;
-  int Hkv;
-  int G;
-  int g_inv;                // 65536 / G + 1: x / G == x * g_inv >> 16 for x < 384, G <= 128
-  int window;               // 0: none
-  int sinks;
-  int k;
-  float c;                  // scale * log2(e)
-  // workspace
-  int4* head;               // [ctas][2]: what each CTA left in parts
-  float* ml;                // [2 ctas][256][2]
-  float* po;                // [2 ctas][256][D]
-  DevCtl ctl;
-};
-
-// ---- units -------------------------------------------------------------------
-
-struct Unit {
-  int b;       // sequence (list form: unused)
-  int m;       // row block (list form: token)
-  int j;       // key head
-  int64_t off; // cost already spent of this unit
-};
-
-struct SeqInfo {
-  int64_t t0;  // first row of the packed batch
-  int n;       // new tokens
-  int len;     // keys
-  int p0;      // position of the first new token
-};
-
-__device__ __forceinline__ SeqInfo seq_info(const AttParams& p, int b) {
-  SeqInfo s;
-  int t0 = __ldg(p.cu_q + b), t1 = __ldg(p.cu_q + b + 1);
-  t0 = min(max(t0, 0), p.n_tok);
-  t1 = min(max(t1, t0), p.n_tok);
-  int64_t len = __ldg(p.lens + b);
-  const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
-  len = len < 0 ? 0 : len > cap ? cap : len;
-  s.t0 = t0;
-  s.n = t1 - t0;
-  s.len = static_cast<int>(len);
-  s.p0 = s.len - s.n;
-  return s;
-}
-
-__device__ __forceinline__ int64_t row_blocks(const AttParams& p, const SeqInfo& s) {
-  return (static_cast<int64_t>(s.n) * p.G + kBlockRows - 1) / kBlockRows;
-}
-
-// Cost of row block m of a sequence and its sum over blocks 0..m-1: about the
-// keys it passes over, times G.  Only the balance depends on it.
-__device__ __forceinline__ int64_t cost_flat(const AttParams& p) {
-  return p.window ? static_cast<int64_t>(p.G) * (static_cast<int64_t>(p.window) + p.sinks + 2 * kTile) +
-                        kBlockRows
-                  : 0x3fffffffffffffffLL;
-}
-__device__ __forceinline__ int64_t cost_of(const AttParams& p, const SeqInfo& s, int64_t m) {
-  const int64_t c = static_cast<int64_t>(p.G) * (max(s.p0, 0) + kTile) + kBlockRows * (m + 1);
-  return min(c, cost_flat(p));
-}
-__device__ __forceinline__ int64_t cost_before(const AttParams& p, const SeqInfo& s, int64_t m) {
-  const int64_t base = static_cast<int64_t>(p.G) * (max(s.p0, 0) + kTile);
-  const int64_t flat = cost_flat(p);
-  // blocks below `lin` grow with m, those from it on cost `flat`
-  int64_t lin = flat > base ? (flat - base) / kBlockRows : 0;
-  lin = min(lin, m);
-  return lin * base + kBlockRows * (lin * (lin + 1) / 2) + (m - lin) * (m > lin ? flat : 0);
-}
-
-// Tiles of a unit: `sink` tiles from the start, then tiles lo.. .
-struct Tiles {
-  int n;     // tiles in all
-  int sink;
-  int lo;
-  int rows;  // valid rows of the unit
-};
-
-__device__ __forceinline__ Tiles unit_tiles(const AttParams& p, const SeqInfo& s, int m) {
-  Tiles t;
-  const int64_t r0 = static_cast<int64_t>(m) * kBlockRows;
-  const int64_t all = static_cast<int64_t>(s.n) * p.G;
-  t.rows = static_cast<int>(min(static_cast<int64_t>(kBlockRows), all - r0));
-  const int p_first = s.p0 + static_cast<int>(r0 / p.G);
-  const int p_last = s.p0 + static_cast<int>((r0 + t.rows - 1) / p.G);
-  const int end = p_last < 0 ? 1 : p_last / kTile + 1;  // a unit that sees nothing passes one tile
-  t.lo = 0;
-  t.sink = 0;
-  if (p.window) {
-    const int64_t f = static_cast<int64_t>(p_first) - p.window + 1;
-    t.lo = f > 0 ? static_cast<int>(f / kTile) : 0;
-    t.sink = min((p.sinks + kTile - 1) / kTile, t.lo);
-  }
-  t.n = t.sink + end - t.lo;
-  return t;
-}
 
 // What the roles work on: tiles [i0, i1) of a unit, whole or a part.  Written to
 // shared memory by the scheduling warp, a few ahead.
@@ -396,11 +278,13 @@ __device__ __forceinline__ int tile_at(const AttParams& p, const Unit& u, int& n
   return static_cast<int>(u.off * t.n / cost_of(p, s, u.m));
 }
 
-// What the CTA will leave in the workspace, for the joining kernel:
-//   head[2 c]     x: 1 if it continues a unit that an earlier CTA opened with at
-//                 least one tile, y: 1 if the unit ends here
-//   head[2 c + 1] x: 1 if it opens a unit that it does not finish, y: sequence
-//                 (list form: 0), z: row block (token), w: key head
+// List form: with 8 units or more for a CTA, units are left whole (the CTAs' work
+// then differs by one unit at most) and nothing has to be joined.
+__host__ __device__ inline bool whole_units(const AttParams& p, int ctas) {
+  return static_cast<int64_t>(p.n_tok) * p.Hkv >= 8ll * ctas;
+}
+
+// What the CTA will leave in the workspace, for the joining kernel.
 template <bool LIST>
 __device__ __forceinline__ void write_head(const AttParams& p, const Start& st, const Unit& end) {
   const int c = blockIdx.x;
@@ -433,25 +317,6 @@ __device__ __forceinline__ void write_head(const AttParams& p, const Start& st, 
   p.head[2 * c + 1] = open;
 }
 
-// ---- small device helpers --------------------------------------------------------
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<const float2*>(&r);
-}
 // The low n bits (n clamped to 0..32).
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
@@ -537,15 +402,17 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   const int warp = warp_id(), lane = lane_id();
+  asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may get ready
 
   Start st;
   if constexpr (LIST) {
     // every unit costs its tiles: the stretch is a division away
     const int64_t nt = (p.k + kTile - 1) / kTile;
-    const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * nt;
     const int64_t n = gridDim.x, c = blockIdx.x;
-    const int64_t x0 = total / n * c + total % n * c / n;
-    const int64_t x1 = total / n * (c + 1) + total % n * (c + 1) / n;
+    const int64_t step = whole_units(p, gridDim.x) ? nt : 1;
+    const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * nt / step;
+    const int64_t x0 = (total / n * c + total % n * c / n) * step;
+    const int64_t x1 = (total / n * (c + 1) + total % n * (c + 1) / n) * step;
     auto unit = [&](int64_t x) {
       const int64_t q = x / nt;
       return Unit{0, static_cast<int>(q / p.Hkv), static_cast<int>(q % p.Hkv), x % nt};
@@ -1075,7 +942,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(g.part) * kBlockRows + r) * 2) =
                 make_float2(m, l);
           } else if (p.lse) {
-            p.lse[orow] = l > 0.0f ? (m + __log2f(l)) * 0.69314718055994530942f : l == 0.0f ? -INFINITY : l;
+            p.lse[orow] = row_lse(m, l);
           }
         }
       }
@@ -1174,145 +1041,32 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   }
 }
 
-// Joins the parts of the unit that CTA blockIdx.x opened and did not finish:
-// o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i, parts in CTA order.  A warp
-// takes a row: its lanes hold the parts' m and l, 32 at a time.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 8;      // blocks in y, 8 rows each at a time
-constexpr int kMaxCtas = 256;
-
-template <int D, bool LIST>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttParams p, int ctas) {
-  __shared__ int parts[kMaxCtas];  // workspace slots of the unit's parts, in order
-  __shared__ int first_end, warp_n[kJoinThreads / 32];
-  const int c = blockIdx.x;
-  const int4 open = p.head[2 * c + 1];
-  if (!open.x) return;
-  int64_t t0;
-  int rows;
-  if constexpr (LIST) {
-    if (open.z >= p.n_tok) return;
-    const int b = __ldg(p.seq_of + open.z);
-    if (b < 0 || b >= p.n_seq) return;
-    t0 = open.z;
-    rows = p.G;
-  } else {
-    const SeqInfo s = seq_info(p, open.y);
-    const Tiles t = unit_tiles(p, s, open.z);
-    t0 = s.t0;
-    rows = t.rows;
-  }
-  if (static_cast<int>(blockIdx.y) * 8 >= rows) return;
-  // the CTAs that follow, up to the one that ends the unit (a CTA whose share
-  // of it is less than a tile has no part)
-  const int e = c + 1 + static_cast<int>(threadIdx.x);
-  const int4 cont = e < ctas ? p.head[2 * e] : make_int4(0, 0, 0, 0);
-  if (threadIdx.x == 0) first_end = ctas;
-  __syncthreads();
-  if (cont.y) atomicMin(&first_end, e);
-  __syncthreads();
-  const bool mine = cont.x && e <= first_end;
-  const uint32_t vote = __ballot_sync(0xffffffffu, mine);
-  if (lane_id() == 0) warp_n[warp_id()] = __popc(vote);
-  __syncthreads();
-  int at = 1, n = 1;
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    if (w < warp_id()) at += warp_n[w];
-    n += warp_n[w];
-  }
-  if (mine) parts[at + __popc(vote & ((1u << lane_id()) - 1u))] = 2 * e;
-  if (threadIdx.x == 0) parts[0] = 2 * c + 1;
-  __syncthreads();
-
-  constexpr int V = D / 32;  // elements of a lane
-  const int lane = lane_id();
-  for (int r = blockIdx.y * 8 + warp_id(); r < rows; r += gridDim.y * 8) {
-    float m = -INFINITY, l = 0.0f, o[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.0f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float pm = -INFINITY, pl = 0.0f;
-      int64_t q = 0;
-      if (i0 + lane < n) {
-        q = static_cast<int64_t>(parts[i0 + lane]) * kBlockRows + r;
-        const float2 x = *reinterpret_cast<const float2*>(p.ml + 2 * q);
-        pm = x.x;
-        pl = x.y;
-      }
-      float top = fmaxf(pm, m);
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      const float ref = top == -INFINITY ? 0.0f : top;
-      const float f0 = ex2(m - ref), f = ex2(pm - ref);
-      float lsum = f * pl;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
-      l = l * f0 + lsum;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] *= f0;
-      m = top;
-      const int left = min(32, n - i0);
-#pragma unroll 4
-      for (int x = 0; x < left; ++x) {
-        const float w = __shfl_sync(0xffffffffu, f, x);
-        const int64_t qx = __shfl_sync(0xffffffffu, q, x);
-        float y[V];
-        if constexpr (V == 4) {
-          const float4 z = *reinterpret_cast<const float4*>(p.po + qx * D + lane * V);
-          y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
-        } else {
-          const float2 z = *reinterpret_cast<const float2*>(p.po + qx * D + lane * V);
-          y[0] = z.x, y[1] = z.y;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = fmaf(w, y[i], o[i]);
-      }
-    }
-    const int64_t rr = (LIST ? 0 : static_cast<int64_t>(open.z) * kBlockRows) + r;
-    const int64_t row = (t0 + rr / p.G) * p.H + open.w * p.G + rr % p.G;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint32_t w[V / 2];
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) w[i] = bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(p.out + row * D + lane * V) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V) = w[0];
-    if (p.lse && lane == 0)
-      p.lse[row] = l > 0.0f ? (m + __log2f(l)) * 0.69314718055994530942f : l == 0.0f ? -INFINITY : l;
-  }
+// Whether any unit can be cut: not where every CTA has whole units of the list form.
+template <bool LIST>
+bool parts_possible(const AttParams& p, int ctas) {
+  if (!LIST) return true;
+  return !whole_units(p, ctas);
 }
-
-int att_ctas() { return std::min(sm_count(), kMaxCtas); }
-
-struct AttWs {
-  size_t head, ml, po, total;
-  explicit AttWs(int d) {
-    const size_t n = static_cast<size_t>(att_ctas());
-    size_t o = 0;
-    head = o;
-    o += (n * 2 * sizeof(int4) + 255) / 256 * 256;
-    ml = o;
-    o += n * 2 * kBlockRows * 2 * sizeof(float);
-    po = o;
-    o += n * 2 * kBlockRows * static_cast<size_t>(d) * sizeof(float);
-    total = o;
-  }
-};
 
 template <int D, bool LIST>
 cudaError_t launch_att(const AttParams& p, const CUtensorMap& km, const CUtensorMap& vm,
                        cudaStream_t s) {
   using L = AttLayout<D, LIST>;
   auto kern = attend_kernel<D, LIST>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+  static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready.fetch_or(uint64_t{1} << dev);
+  }
   const int n = att_ctas();
   kern<<<n, L::THREADS, L::ALLOC, s>>>(km, vm, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  join_kernel<D, LIST><<<dim3(n, kJoinRows), kJoinThreads, 0, s>>>(p, n);
-  return cudaGetLastError();
+  if (e != cudaSuccess || !parts_possible<LIST>(p, n)) return e;
+  return launch_join<D, LIST>(p, n, kBlockRows, kJoinRows, s);
 }
 
 }  // namespace
@@ -1320,41 +1074,11 @@ cudaError_t launch_att(const AttParams& p, const CUtensorMap& km, const CUtensor
 size_t attend_workspace(int d) { return AttWs(d).total; }
 
 cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
-  AttParams p{};
-  p.Q = a.Q;
-  p.kp = a.k_pages;
-  p.vp = a.v_pages;
-  p.bts = a.block_tables;
-  p.cu_q = a.cu_q;
-  p.lens = a.seq_lens;
-  p.seq_of = a.seq_of;
-  p.positions = a.positions;
-  p.idx = a.idx;
-  p.out = a.out;
-  p.lse = a.lse;
-  p.n_pages = a.n_pages;
-  p.key_rows = a.n_pages << a.page_shift;
-  p.max_blocks = a.max_blocks;
-  p.page_shift = a.page_shift;
-  p.n_seq = a.n_seq;
-  p.n_tok = a.n_tok;
-  p.H = a.H;
-  p.Hkv = a.Hkv;
-  p.G = a.H / a.Hkv;
-  p.g_inv = 65536 / p.G + 1;
-  p.window = a.window;
-  p.sinks = a.sinks;
-  p.k = a.k;
-  p.c = a.scale * 1.44269504088896340736f;
-  p.ctl = ctl;
-  const AttWs w(a.d);
-  uint8_t* base = static_cast<uint8_t*>(a.ws);
-  p.head = reinterpret_cast<int4*>(base + w.head);
-  p.ml = reinterpret_cast<float*>(base + w.ml);
-  p.po = reinterpret_cast<float*>(base + w.po);
+  const AttParams p = att_params(a, ctl);
   CUtensorMap km, vm;
   std::memset(&km, 0, sizeof km);
   std::memset(&vm, 0, sizeof vm);
+  if (a.idx && p.G <= kRowHeads) return launch_attend_rows(a, ctl, s);
   if (a.idx) return a.d == 128 ? launch_att<128, true>(p, km, vm, s) : launch_att<64, true>(p, km, vm, s);
   const uint64_t dims[3] = {static_cast<uint64_t>(a.d), static_cast<uint64_t>(a.Hkv),
                             static_cast<uint64_t>(p.key_rows)};

@@ -75,7 +75,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int half = p.r >> 1;
   const int u = threadIdx.x % UPR;
   const int rows = nt * nh;
-  constexpr int RPP = kRopeThreads / UPR;  // rows per pass
   const bool values = PAGED && blockIdx.z == 1;
   const uint16_t* src = values ? p.v : p.x;
 
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   int tok[kUnits];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const int row = i * RPP + threadIdx.x / UPR;
+    const int row = (threadIdx.x / UPR) * kUnits + i;  // heads of one token, mostly
     dst[i] = -1;
     tok[i] = 0;
     in[i] = make_uint4(0, 0, 0, 0);
@@ -130,17 +129,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const int first = p.offset >> 3, units = p.r >> 3;  // rotated units of a row
   const bool turned = u >= first && u < first + units;
   const int lane = lane_id();
+  // this lane's pairs: 4 of its own unit (interleaved), or 8 shared with the unit
+  // of the other half, units / 2 lanes up or down in the same row
+  constexpr int NP = PAIRED ? 4 : 8;
+  const bool low = u - first < (units >> 1);
+  const int other = turned ? lane + (low ? (units >> 1) : -(units >> 1)) : lane;
+  const int pi = turned ? (PAIRED ? u - first : u - first - (low ? 0 : (units >> 1))) * NP : 0;
+  float cc[NP], ss[NP];
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
+    if (i == 0 || tok[i] != tok[i - 1]) {
+      const float* cs = smem_cs + tok[i] * p.r + pi;
+#pragma unroll
+      for (int j = 0; j < NP; j += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(cs + j);
+        const float4 s = *reinterpret_cast<const float4*>(cs + half + j);
+        cc[j] = c.x, cc[j + 1] = c.y, cc[j + 2] = c.z, cc[j + 3] = c.w;
+        ss[j] = s.x, ss[j + 1] = s.y, ss[j + 2] = s.z, ss[j + 3] = s.w;
+      }
+    }
     float e[8] = {bf_lo(in[i].x), bf_hi(in[i].x), bf_lo(in[i].y), bf_hi(in[i].y),
                   bf_lo(in[i].z), bf_hi(in[i].z), bf_lo(in[i].w), bf_hi(in[i].w)};
-    const float* cs = smem_cs + tok[i] * p.r;
     if constexpr (PAIRED) {
       if (turned) {
-        const int pi = (u - first) * 4;
-        const float4 c = *reinterpret_cast<const float4*>(cs + pi);
-        const float4 s = *reinterpret_cast<const float4*>(cs + half + pi);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float a = e[2 * j], b = e[2 * j + 1];
@@ -149,9 +160,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         }
       }
     } else {
-      // the other half of each pair: units / 2 lanes up or down in the same row
-      const bool low = u - first < (units >> 1);
-      const int other = turned ? lane + (low ? (units >> 1) : -(units >> 1)) : lane;
       uint4 o;
       o.x = __shfl_sync(0xffffffffu, in[i].x, other);
       o.y = __shfl_sync(0xffffffffu, in[i].y, other);
@@ -160,21 +168,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       if (turned) {
         const float f[8] = {bf_lo(o.x), bf_hi(o.x), bf_lo(o.y), bf_hi(o.y),
                             bf_lo(o.z), bf_hi(o.z), bf_lo(o.w), bf_hi(o.w)};
-        const int pi = (u - first - (low ? 0 : (units >> 1))) * 8;
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(cs + pi + j);
-          const float4 s = *reinterpret_cast<const float4*>(cs + half + pi + j);
-          const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            e[j + q] = low ? e[j + q] * cc[q] - f[j + q] * ss[q] : f[j + q] * ss[q] + e[j + q] * cc[q];
-        }
+        for (int j = 0; j < 8; ++j)  // a cos - b sin, or b cos + a sin
+          e[j] = e[j] * cc[j] + f[j] * (low ? -ss[j] : ss[j]);
       }
     }
     if constexpr (F8) {
       // scale = largest magnitude / 448 (1 for a row of zeros); codes rounded to
-      // nearest even from the 32-bit rotated values
+      // nearest even from the 32-bit rotated values times 1 / scale: within 2^-23
+      // of the quotient, so a code differs from the quotient's only next to a tie
+      // (eight divisions a lane took 87 us where one takes 41 on 8192 x 64 x 128)
       float m = 0.0f;
       bool bad = false;
 #pragma unroll
@@ -189,10 +192,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       if (dst[i] >= 0) {
         if (bad) report(p.ctl, DEV_BAD_INPUT);
         uint2 w;
-        const uint32_t q0 = pack_e4m3(e[0] / scale, e[1] / scale);
-        const uint32_t q1 = pack_e4m3(e[2] / scale, e[3] / scale);
-        const uint32_t q2 = pack_e4m3(e[4] / scale, e[5] / scale);
-        const uint32_t q3 = pack_e4m3(e[6] / scale, e[7] / scale);
+        const float inv = fminf(1.0f / scale, 3.402823466e38f);  // (finite for the smallest scales)
+        const uint32_t q0 = pack_e4m3(e[0] * inv, e[1] * inv);
+        const uint32_t q1 = pack_e4m3(e[2] * inv, e[3] * inv);
+        const uint32_t q2 = pack_e4m3(e[4] * inv, e[5] * inv);
+        const uint32_t q3 = pack_e4m3(e[6] * inv, e[7] * inv);
         w.x = q0 | (q1 << 16);
         w.y = q2 | (q3 << 16);
         *reinterpret_cast<uint2*>(p.y8 + dst[i] * D + u * 8) = w;

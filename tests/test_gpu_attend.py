@@ -274,7 +274,7 @@ def test_attend_in_a_graph_and_beside_another_stream(lib):
 
 def test_expired_waits_report_timeout(lib):
     # enough rows that the loaders wait on the products for several microseconds
-    cache, Q, cu, ln, seqs, pos = _batch([256] * 2, [9000] * 2, 32, 2, 128, 64, seed=47)
+    cache, Q, cu, ln, seqs, pos = _batch([128] * 2, [9000] * 2, 64, 2, 128, 64, seed=47)
     ref, rlse = _run(lib, cache, Q, cu, ln)
     i32 = lambda x: torch.as_tensor(np.ascontiguousarray(x), dtype=torch.int32, device="cuda")
     idx = i32(_lists(pos, 1500, 3))
