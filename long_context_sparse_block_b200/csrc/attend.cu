@@ -73,16 +73,17 @@ struct AttLayout {
 // shared memory by the scheduling warp, a few ahead.
 struct __align__(16) Seg {
   int valid;   // 0: the end
-  int t0;      // first row of the sequence in the packed batch (list form: the token)
   int len;     // keys of the sequence
-  int p0;      // position of the first new token (list form: of the token)
+  int p0;      // position of the unit's first token
+  int pad0;
   int b, m, j;
   int i0, i1;
   int part;    // workspace slot, or -1: the whole unit
   int split;   // both slots share the rows (alternate tiles)
-  int rows;    // valid rows of the unit
+  int toks;    // tokens of the unit
+  int tb;      // its first token in the packed batch
   int sink, lo;
-  int tb, rem; // row m * 256 is query tb of the sequence, head rem of the group
+  int pad;
   __device__ __forceinline__ int key0(int i) const { return (i < sink ? i : lo + i - sink) * kTile; }
   // tiles of a slot
   __device__ __forceinline__ int tiles_of(int slot) const {
@@ -96,6 +97,8 @@ static_assert(sizeof(Seg) == 64, "segment slot");
 struct Start {
   Unit u;
   int64_t left;
+  int64_t x1, total;  // its end on the line, and the line's
+  int workers;        // CTAs that share it
 };
 
 template <bool LIST>
@@ -131,11 +134,11 @@ struct Walk {
           report(p.ctl, DEV_BAD_INPUT);
           continue;
         }
-        g.t0 = g.m;
+        g.tb = g.m;
         g.p0 = __ldg(p.positions + g.m);
         g.len = 0;
-        g.rows = p.G;
-        g.sink = g.lo = g.tb = g.rem = 0;
+        g.toks = 1;
+        g.sink = g.lo = 0;
         g.split = 1;
         g.part = g.i0 > 0 ? 2 * cta : g.i1 < nt ? 2 * cta + 1 : -1;
         g.valid = 1;
@@ -150,8 +153,8 @@ struct Walk {
         const Tiles t = unit_tiles(p, s, u.m);
         const int64_t cost = cost_of(p, s, u.m);
         const int64_t end = min(cost, u.off + left);
-        g.i0 = static_cast<int>(u.off * t.n / cost);
-        g.i1 = static_cast<int>(end * t.n / cost);
+        g.i0 = tile_of(u.off, cost, t.n);
+        g.i1 = tile_of(end, cost, t.n);
         g.b = u.b;
         g.m = u.m;
         g.j = u.j;
@@ -165,16 +168,13 @@ struct Walk {
           }
         }
         if (g.i1 <= g.i0) continue;
-        g.t0 = static_cast<int>(s.t0);
+        g.tb = static_cast<int>(s.t0) + g.m * 2 * p.T;
         g.len = s.len;
-        g.p0 = s.p0;
-        g.rows = t.rows;
+        g.p0 = s.p0 + g.m * 2 * p.T;
+        g.toks = t.toks;
         g.sink = t.sink;
         g.lo = t.lo;
-        const int64_t r0 = static_cast<int64_t>(g.m) * kBlockRows;
-        g.tb = static_cast<int>(r0 / p.G);
-        g.rem = static_cast<int>(r0 % p.G);
-        g.split = t.rows <= kTile;
+        g.split = t.toks <= p.T;
         g.part = g.i0 > 0 ? 2 * cta : g.i1 < t.n ? 2 * cta + 1 : -1;
         g.valid = 1;
         return;
@@ -183,10 +183,8 @@ struct Walk {
   }
 };
 
-// All threads: finds the unit at point x of the line (x in [0, total)).  Called
-// with the block's prefix of sequence costs in hand.
-__device__ __forceinline__ void locate(const AttParams& p, int b, int64_t x, Unit& u) {
-  const SeqInfo s = seq_info(p, b);
+// The unit at point x of a sequence's costs.
+__device__ __forceinline__ Unit locate(const AttParams& p, const SeqInfo& s, int b, int64_t x) {
   int64_t lo = 0, hi = row_blocks(p, s) - 1;
   while (lo < hi) {  // the last block that starts at or before x
     const int64_t mid = (lo + hi + 1) >> 1;
@@ -197,85 +195,91 @@ __device__ __forceinline__ void locate(const AttParams& p, int b, int64_t x, Uni
   }
   x -= cost_before(p, s, lo) * p.Hkv;
   const int64_t c = cost_of(p, s, lo);
-  u.b = b;
-  u.m = static_cast<int>(lo);
-  u.j = static_cast<int>(x / c);
-  u.off = x % c;
+  int j = 0;
+  for (; x >= c; ++j) x -= c;
+  return Unit{b, static_cast<int>(lo), j, x};
 }
 
 struct PlanShared {
   Unit at[2];       // the units at the two ends of the stretch
-  int64_t ends[2];
   int64_t warp_sum[16];
-  int64_t carry;
 };
 
-// Scans the sequences' costs and finds this CTA's stretch [total c / n, total
-// (c + 1) / n).  Two passes over the sequences when the threads do not hold them
-// all (their lengths are in cache by then).
+// Finds the CTA's stretch of the line, cut(total, c) to cut(total, c + 1):
+// a block scan of the sequences' costs, again for the units when the threads do
+// not hold all sequences.
 template <int THREADS>
 __device__ __forceinline__ void plan_stretch(const AttParams& p, PlanShared& ps, Start& st) {
   const int tid = threadIdx.x;
-  int64_t total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t carry = 0;
-    int64_t x0 = 0, x1 = 0;
-    if (pass == 1) {
-      const int64_t n = gridDim.x, c = blockIdx.x;
-      x0 = total / n * c + total % n * c / n;
-      x1 = total / n * (c + 1) + total % n * (c + 1) / n;
-      if (tid == 0) {
-        ps.ends[0] = x0;
-        ps.ends[1] = x1;
-        ps.at[0] = Unit{p.n_seq, 0, 0, 0};
-        ps.at[1] = Unit{p.n_seq, 0, 0, 0};
-      }
+  if (tid < 2) ps.at[tid] = Unit{p.n_seq, 0, 0, 0};
+  int64_t total = 0, x0 = 0, x1 = 0;
+  SeqInfo s{};
+  int64_t cost = 0, first = 0;
+  // cost and first point of sequence base + tid; total grows by the chunk's costs
+  auto scan = [&](int base) {
+    const int b = base + tid;
+    cost = 0;
+    if (b < p.n_seq) {
+      s = seq_info(p, b);
+      if (s.n > 0) cost = cost_before(p, s, row_blocks(p, s)) * p.Hkv;
     }
-    for (int base = 0; base < p.n_seq; base += THREADS) {
-      const int b = base + tid;
-      int64_t cost = 0;
-      if (b < p.n_seq) {
-        const SeqInfo s = seq_info(p, b);
-        if (pass == 0) {
-          const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
-          const int len = __ldg(p.lens + b);
-          if (len < 0 || len > cap) report(p.ctl, DEV_BAD_INPUT);
-        }
-        if (s.n > 0) cost = cost_before(p, s, row_blocks(p, s)) * p.Hkv;
-      }
-      int64_t x = cost;
+    int64_t x = cost;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane_id() >= o) x += y;
-      }
-      __syncthreads();
-      if (lane_id() == 31) ps.warp_sum[warp_id()] = x;
-      __syncthreads();
-      int64_t before = carry;
-      for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp_id()) before += ps.warp_sum[w];
-        carry += ps.warp_sum[w];
-      }
-      if (pass == 1 && cost > 0) {
-        const int64_t lo = before + x - cost, hi = before + x;
-        if (x0 >= lo && x0 < hi) locate(p, b, x0 - lo, ps.at[0]);
-        if (x1 >= lo && x1 < hi) locate(p, b, x1 - lo, ps.at[1]);
-      }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane_id() >= o) x += y;
     }
-    total = carry;
     __syncthreads();
+    if (lane_id() == 31) ps.warp_sum[warp_id()] = x;
+    __syncthreads();
+    first = total + x - cost;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const int64_t v = ps.warp_sum[w];
+      if (w < warp_id()) first += v;
+      total += v;
+    }
+  };
+  auto find = [&](int base) {
+    if (x0 >= first && x0 < first + cost) ps.at[0] = locate(p, s, base + tid, x0 - first);
+    if (x1 >= first && x1 < first + cost) ps.at[1] = locate(p, s, base + tid, x1 - first);
+  };
+  for (int base = 0; base < p.n_seq; base += THREADS) {
+    scan(base);
+    const int b = base + tid;
+    if (blockIdx.x == 0 && b < p.n_seq) {
+      const int len = __ldg(p.lens + b);
+      if (len < 0 || len > (static_cast<int64_t>(p.max_blocks) << p.page_shift))
+        report(p.ctl, DEV_BAD_INPUT);
+    }
   }
+  const int64_t all = total;
+  // a stretch is worth two tiles at least: shorter ones only add parts to join
+  st.workers = static_cast<int>(min(static_cast<int64_t>(p.workers), max(all >> 8, int64_t{1})));
+  const int c = min(static_cast<int>(blockIdx.x), st.workers);
+  x0 = cut(p, st.workers, all, c);
+  x1 = cut(p, st.workers, all, min(c + 1, st.workers));
+  if (p.n_seq <= THREADS) {
+    find(0);
+  } else {
+    total = 0;
+    for (int base = 0; base < p.n_seq; base += THREADS) {
+      scan(base);
+      find(base);
+    }
+  }
+  __syncthreads();
   st.u = ps.at[0];
-  st.left = ps.ends[1] - ps.ends[0];
+  st.left = x1 - x0;
+  st.x1 = x1;
+  st.total = all;
 }
 
 // Tile boundary of a unit at cost offset `off`.
 __device__ __forceinline__ int tile_at(const AttParams& p, const Unit& u, int& n) {
   const SeqInfo s = seq_info(p, u.b);
-  const Tiles t = unit_tiles(p, s, u.m);
-  n = t.n;
-  return static_cast<int>(u.off * t.n / cost_of(p, s, u.m));
+  n = unit_tiles(p, s, u.m).n;
+  return tile_of(u.off, cost_of(p, s, u.m), n);
 }
 
 // List form: with 8 units or more for a CTA, units are left whole (the CTAs' work
@@ -289,29 +293,39 @@ template <bool LIST>
 __device__ __forceinline__ void write_head(const AttParams& p, const Start& st, const Unit& end) {
   const int c = blockIdx.x;
   int4 cont = make_int4(0, 0, 0, 0), open = make_int4(0, 0, 0, 0);
-  const int past = LIST ? p.n_tok : p.n_seq;
-  const int key_s = LIST ? st.u.m : st.u.b, key_e = LIST ? end.m : end.b;
+  const int nl = (p.k + kTile - 1) / kTile;
   const bool same = st.u.b == end.b && st.u.m == end.m && st.u.j == end.j;
-  int i0 = 0, i1 = 0, n = 0;
-  if (key_s < past) {
-    if (LIST) {
-      n = (p.k + kTile - 1) / kTile;
-      i0 = static_cast<int>(st.u.off);
-    } else {
-      i0 = tile_at(p, st.u, n);
-    }
-    if (i0 > 0) {
-      int n2;
-      i1 = !same ? n : LIST ? static_cast<int>(end.off) : tile_at(p, end, n2);
-      cont.x = i1 > i0;
-      cont.y = i1 >= n;
-    }
+  auto past = [&](const Unit& u) { return LIST ? u.m >= p.n_tok : u.b >= p.n_seq; };
+  auto tile = [&](const Unit& u, int& n) {
+    if (!LIST) return tile_at(p, u, n);
+    n = nl;
+    return static_cast<int>(u.off);
+  };
+  int i0 = 0, n = 0;
+  if (!past(st.u)) i0 = tile(st.u, n);
+  if (i0 > 0) {
+    int n2;
+    cont.x = (same ? tile(end, n2) : n) > i0;
   }
-  if (key_e < past && end.off > 0 && !(same && i0 > 0) && st.left > 0) {
-    int n2 = (p.k + kTile - 1) / kTile;
-    const int e = LIST ? static_cast<int>(end.off) : tile_at(p, end, n2);
-    if (e > 0 && e < n2) open = make_int4(1, LIST ? 0 : end.b, end.m, end.j);
-    // (e == n2: whole; the row of no sequence of the list form is skipped by all)
+  if (st.left > 0 && !past(end) && end.off > 0 && !(same && i0 > 0)) {
+    int n2;
+    const int e = tile(end, n2);
+    if (e > 0 && e < n2) {  // (e == n2: whole)
+      int tok = end.m, toks = 1;
+      int64_t cost = nl;
+      bool there = true;
+      if constexpr (LIST) {
+        const int b = __ldg(p.seq_of + end.m);
+        there = b >= 0 && b < p.n_seq;  // (else: left as it was)
+      } else {
+        const SeqInfo s = seq_info(p, end.b);
+        tok = static_cast<int>(s.t0) + end.m * 2 * p.T;
+        toks = unit_tiles(p, s, end.m).toks;
+        cost = cost_of(p, s, end.m);
+      }
+      if (there)
+        open = make_int4(1, tok, toks | end.j << 16, last_worker(p, st.workers, st.total, st.x1 - end.off + cost));
+    }
   }
   p.head[2 * c] = cont;
   p.head[2 * c + 1] = open;
@@ -328,6 +342,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
+}
+// Keeps uses of registers that a TMEM load wrote behind the wait before it.
+template <int N>
+__device__ __forceinline__ void tmem_hold_regs(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -381,8 +401,8 @@ __device__ __forceinline__ bool elect_one() {
 
 template <int D, bool LIST>
 __global__ void __launch_bounds__(AttLayout<D, LIST>::THREADS, 1)
-attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-              const AttParams p) {
+attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+              const __grid_constant__ CUtensorMap vmap, const AttParams p) {
   using L = AttLayout<D, LIST>;
   constexpr int ST = L::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -404,33 +424,12 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
   const int warp = warp_id(), lane = lane_id();
   asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may get ready
 
-  Start st;
-  if constexpr (LIST) {
-    // every unit costs its tiles: the stretch is a division away
-    const int64_t nt = (p.k + kTile - 1) / kTile;
-    const int64_t n = gridDim.x, c = blockIdx.x;
-    const int64_t step = whole_units(p, gridDim.x) ? nt : 1;
-    const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * nt / step;
-    const int64_t x0 = (total / n * c + total % n * c / n) * step;
-    const int64_t x1 = (total / n * (c + 1) + total % n * (c + 1) / n) * step;
-    auto unit = [&](int64_t x) {
-      const int64_t q = x / nt;
-      return Unit{0, static_cast<int>(q / p.Hkv), static_cast<int>(q % p.Hkv), x % nt};
-    };
-    st.u = unit(x0);
-    st.left = x1 - x0;
-    if (threadIdx.x == 0) write_head<true>(p, st, unit(x1));
-  } else {
-    plan_stretch<L::THREADS>(p, ps, st);
-    if (threadIdx.x == 0) write_head<false>(p, st, ps.at[1]);
-  }
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(bar(FULL + i), LIST ? 128 : 1);
       mbar_init(bar(EMPTY + i), 1);
     }
-    mbar_init(bar(QFULL), 32);
+    mbar_init(bar(QFULL), 1);
     mbar_init(bar(QEMPTY), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(SFULL + i), 1);
@@ -453,10 +452,35 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       tma_prefetch_desc(&kmap);
       tma_prefetch_desc(&vmap);
     }
+    tma_prefetch_desc(&qmap);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
+  }
+  Start st;
+  Unit end;  // the unit in which the next CTA's stretch begins
+  if constexpr (LIST) {
+    // every unit costs its tiles: the stretch is a division away
+    const int nt = (p.k + kTile - 1) / kTile;
+    const int64_t step = whole_units(p, p.workers) ? nt : 1;
+    const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * (nt / step);
+    const int64_t x0 = cut(p, p.workers, total, blockIdx.x) * step;
+    const int64_t x1 = cut(p, p.workers, total, blockIdx.x + 1) * step;
+    auto unit = [&](int64_t x) {
+      const int64_t q = x / nt;
+      const int t = static_cast<int>(q / p.Hkv);
+      return Unit{0, t, static_cast<int>(q - static_cast<int64_t>(t) * p.Hkv), x - q * nt};
+    };
+    st.u = unit(x0);
+    st.left = x1 - x0;
+    st.x1 = x1;
+    st.total = total * step;
+    st.workers = p.workers;
+    end = unit(x1);
+  } else {
+    plan_stretch<L::THREADS>(p, ps, st);
+    end = ps.at[1];
   }
   tc_fence_before();
   __syncthreads();
@@ -617,7 +641,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       };
       ok = wait(QFULL, sg & 1);
       if (!ok) break;
-      fence_proxy_async_smem();  // the query rows' copies -> MMA operand reads
+      tc_fence_after();
       if (split) {
         for (int x = -2; x < n && ok; ++x) {
           const int slot = x & 1;
@@ -685,6 +709,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         walk.next(p, g);
         segs[sg % kSegs] = g;
         mbar_arrive(bar(GFULL + sg % kSegs));
+        if (sg == 0) write_head<LIST>(p, st, end);
         if (!g.valid) break;
       }
     }
@@ -699,17 +724,19 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (lane == 0) seg_done(sg);
       const int n = g.i1 - g.i0;
       if (!warp_wait(bar(QEMPTY), (sg & 1) ^ 1, abort_flag, p.ctl)) break;
-      // only the rows that exist: what the others hold stays in their own rows of S
-      constexpr int UPR = D / 8;
-      const int u = lane % UPR;
-      const uint16_t* src = p.Q + (static_cast<int64_t>(g.t0 + g.tb) * p.H + g.j * p.G) * D + u * 8;
-#pragma unroll 4
-      for (int r = lane / UPR; r < g.rows; r += 32 / UPR) {
-        const int x = r + g.rem, q = x * p.g_inv >> 16;
-        cp_async16(sQ + (r / kTile) * L::QTILE + (u / 8) * L::CHUNK + swz_offset(r % kTile, u % 8, 128),
-                   src + (static_cast<int64_t>(q) * p.H + (x - q * p.G)) * D, 16u);
+      // a slot's T tokens x G heads as one box per 64 elements; tokens past the
+      // unit's belong to others and stay in their own rows of S
+      if (lane == 0) {
+        if (sg == 0) fence_proxy_async_smem();  // the plan's words lay where the rows go
+        const int slots = g.split ? 1 : 2, toks = LIST ? 1 : p.T;
+        mbar_arrive_expect_tx(bar(QFULL), slots * L::CH * toks * p.G * 128);
+        for (int i = 0; i < slots; ++i)
+#pragma unroll
+          for (int c = 0; c < L::CH; ++c)
+            tma_load_3d(sQ + i * L::QTILE + c * L::CHUNK, &qmap, bar(QFULL), c * 64, g.j * p.G,
+                        g.tb + i * p.T);
       }
-      cp_async_mbar_arrive_noinc(bar(QFULL));
+      __syncwarp();
       const int key0 = g.key0(g.i1 - 1);
       if (!LIST && g.len > key0 && g.len < key0 + kTile) {
         // the last tile's value rows past the end of the sequence
@@ -749,15 +776,12 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (!__all_sync(0xffffffffu, seg_wait(sg))) break;
       const Seg& g = seg_at(sg);
       const int n = g.tiles_of(slot);
-      const int r = (g.split ? 0 : slot * kTile) + row;  // row of the unit
-      const bool live = r < g.rows;
-      const bool warp_live = (r & ~31) < g.rows;
-      int pos;
-      if constexpr (LIST) {
-        pos = g.p0;
-      } else {
-        pos = live ? g.p0 + g.tb + ((r + g.rem) * p.g_inv >> 16) : -1;
-      }
+      // row of the slot: query `tok` of the unit, head hd of the group
+      const int tok0 = g.split ? 0 : slot * p.T;
+      const int tr = row * p.g_inv >> 16, hd = row - tr * p.G, tok = tok0 + tr;
+      const bool live = tr < p.T && tok < g.toks;
+      const bool warp_live = (row & ~31) < min(p.T, g.toks - tok0) * p.G;
+      const int pos = LIST ? g.p0 : live ? g.p0 + tok : -1;
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < n; ++i) {
         const int x = g.i0 + (g.split ? 2 * i + slot : i);
@@ -791,8 +815,9 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
           uint32_t v[4][32];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, v[q]);
+          tmem_wait_ld_regs(v[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_wait_ld_regs(v[q]);
+          for (int q = 1; q < 4; ++q) tmem_hold_regs(v[q]);
           if ((w[0] & w[1] & w[2] & w[3]) != 0xffffffffu) {
 #pragma unroll
             for (int q = 0; q < 128; ++q)
@@ -833,10 +858,10 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
             for (int q = 0; q < 16; ++q) {
               const float2 z = fma2(make_float2(__uint_as_float(v[q0][2 * q]),
                                                 __uint_as_float(v[q0][2 * q + 1])), cc, nr);
-              const float e0 = ex2(z.x), e1 = ex2(z.y);
-              v[q0][2 * q] = __float_as_uint(e0);
-              v[q0][2 * q + 1] = __float_as_uint(e1);
-              o[q] = bf16x2(e0, e1);
+              const float2 e = make_float2(ex2(z.x), ex2(z.y));
+              v[q0][2 * q] = __float_as_uint(e.x);
+              v[q0][2 * q + 1] = __float_as_uint(e.y);
+              o[q] = bf16x2(e.x, e.y);
             }
             tmem_st16(tS + q0 * 16, o);
             if (q0 & 1) {  // half of P is there: its products can start
@@ -866,9 +891,8 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
       if (!ok) break;
 
       // ---- the segment's result
-      const int rq = (r + g.rem) * p.g_inv >> 16;
-      const int64_t orow =
-          static_cast<int64_t>(g.t0 + g.tb + rq) * p.H + g.j * p.G + (r + g.rem - rq * p.G);
+      const int64_t orow = static_cast<int64_t>(g.tb + tok) * p.H + g.j * p.G + hd;
+      const int r = (g.split ? 0 : slot * kTile) + row;  // workspace row
       if (g.split && slot == 1) {
         // (m, l) to slot 0, which joins the two halves of the tiles
         ok = warp_wait(bar(MLEMPTY), (segs_split & 1) ^ 1, abort_flag, p.ctl);
@@ -906,7 +930,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         const bool join = g.split && n1 > 0;
         const float inv = g.part >= 0 ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
         const float a0 = f0 * inv, a1 = f1 * inv;
-        float* part_o = p.po + (static_cast<int64_t>(g.part) * kBlockRows + r) * D;
+        float* part_o = p.po + (static_cast<int64_t>(g.part) * kPartRows + r) * D;
         uint16_t* dst = p.out + orow * D;
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -939,7 +963,7 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
         }
         if (live) {
           if (g.part >= 0) {
-            *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(g.part) * kBlockRows + r) * 2) =
+            *reinterpret_cast<float2*>(p.ml + (static_cast<int64_t>(g.part) * kPartRows + r) * 2) =
                 make_float2(m, l);
           } else if (p.lse) {
             p.lse[orow] = row_lse(m, l);
@@ -1032,7 +1056,6 @@ attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ 
     }
   }
 
-  if (warp == 2) cp_async_wait_all();
   __syncthreads();
   if (*abort_flag) drain_pause(kDrainNs);  // let issued copies / MMAs land
   if (warp == 1) {
@@ -1049,8 +1072,8 @@ bool parts_possible(const AttParams& p, int ctas) {
 }
 
 template <int D, bool LIST>
-cudaError_t launch_att(const AttParams& p, const CUtensorMap& km, const CUtensorMap& vm,
-                       cudaStream_t s) {
+cudaError_t launch_att(const AttParams& p, const CUtensorMap& qm, const CUtensorMap& km,
+                       const CUtensorMap& vm, cudaStream_t s) {
   using L = AttLayout<D, LIST>;
   auto kern = attend_kernel<D, LIST>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
@@ -1062,11 +1085,11 @@ cudaError_t launch_att(const AttParams& p, const CUtensorMap& km, const CUtensor
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(uint64_t{1} << dev);
   }
-  const int n = att_ctas();
-  kern<<<n, L::THREADS, L::ALLOC, s>>>(km, vm, p);
+  const int n = p.workers;
+  kern<<<n, L::THREADS, L::ALLOC, s>>>(qm, km, vm, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || !parts_possible<LIST>(p, n)) return e;
-  return launch_join<D, LIST>(p, n, kBlockRows, kJoinRows, s);
+  return launch_join<D>(p, kPartRows, kJoinBlocks, s);
 }
 
 }  // namespace
@@ -1074,12 +1097,24 @@ cudaError_t launch_att(const AttParams& p, const CUtensorMap& km, const CUtensor
 size_t attend_workspace(int d) { return AttWs(d).total; }
 
 cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
-  const AttParams p = att_params(a, ctl);
-  CUtensorMap km, vm;
+  const int64_t tiles = a.idx ? static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kTile - 1) / kTile)
+                              : att_ctas();
+  const AttParams p =
+      att_params(a, ctl, static_cast<int>(std::min<int64_t>(att_ctas(), tiles)));
+  if (a.idx && p.G <= kRowHeads) return launch_attend_rows(a, ctl, s);
+  CUtensorMap qm, km, vm;
   std::memset(&km, 0, sizeof km);
   std::memset(&vm, 0, sizeof vm);
-  if (a.idx && p.G <= kRowHeads) return launch_attend_rows(a, ctl, s);
-  if (a.idx) return a.d == 128 ? launch_att<128, true>(p, km, vm, s) : launch_att<64, true>(p, km, vm, s);
+  const uint64_t qdims[3] = {static_cast<uint64_t>(a.d), static_cast<uint64_t>(a.H),
+                             static_cast<uint64_t>(a.n_tok)};
+  const uint64_t qstrides[2] = {static_cast<uint64_t>(a.d) * 2,
+                                static_cast<uint64_t>(a.d) * 2 * static_cast<uint64_t>(a.H)};
+  const uint32_t qbox[3] = {64, static_cast<uint32_t>(p.G), a.idx ? 1u : static_cast<uint32_t>(p.T)};
+  if (encode_tensor_map(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.Q, qdims, qstrides, qbox,
+                        CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  if (a.idx)
+    return a.d == 128 ? launch_att<128, true>(p, qm, km, vm, s) : launch_att<64, true>(p, qm, km, vm, s);
   const uint64_t dims[3] = {static_cast<uint64_t>(a.d), static_cast<uint64_t>(a.Hkv),
                             static_cast<uint64_t>(p.key_rows)};
   const uint64_t strides[2] = {static_cast<uint64_t>(a.d) * 2,
@@ -1090,7 +1125,8 @@ cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t
       encode_tensor_map(&vm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.v_pages, dims, strides, box,
                         CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  return a.d == 128 ? launch_att<128, false>(p, km, vm, s) : launch_att<64, false>(p, km, vm, s);
+  return a.d == 128 ? launch_att<128, false>(p, qm, km, vm, s)
+                    : launch_att<64, false>(p, qm, km, vm, s);
 }
 
 }  // namespace misa

@@ -11,7 +11,7 @@ namespace misa {
 namespace {
 
 constexpr int kTile = 128;       // keys per tile of the dense form
-constexpr int kBlockRows = 256;  // rows of a unit (two slots of 128)
+constexpr int kPartRows = 256;   // workspace rows of a part (two slots of 128)
 constexpr float kRaise = 8.0f;   // log2 of the largest weight before m is raised
 constexpr int kMaxCtas = 256;
 constexpr int kRowHeads = 16;    // list form: query heads of a key head that the row kernel takes
@@ -37,11 +37,14 @@ struct AttParams {
   int H;
   int Hkv;
   int G;
+  int T;                    // tokens of a slot: 128 / G
   int g_inv;                // 65536 / G + 1: x / G == x * g_inv >> 16 for x < 384, G <= 128
   int window;               // 0: none
   int sinks;
   int k;
   float c;                  // scale * log2(e)
+  int workers;              // CTAs (row kernel: warps) that share the line
+  uint64_t w_inv;           // 2^64 / workers + 1
   // workspace
   int4* head;               // [ctas][2]: what each CTA left in parts
   float* ml;                // [2 ctas][256][2]
@@ -80,28 +83,29 @@ __device__ __forceinline__ SeqInfo seq_info(const AttParams& p, int b) {
   return s;
 }
 
+// A unit's rows are the G heads of 2 T tokens: two slots of T tokens, head by head.
 __device__ __forceinline__ int64_t row_blocks(const AttParams& p, const SeqInfo& s) {
-  return (static_cast<int64_t>(s.n) * p.G + kBlockRows - 1) / kBlockRows;
+  return (static_cast<int64_t>(s.n) + 2 * p.T - 1) / (2 * p.T);
 }
 
-// Cost of row block m of a sequence and its sum over blocks 0..m-1: about the
-// keys it passes over, times G.  Only the balance depends on it.
+// Cost of block m of a sequence and its sum over blocks 0..m-1: about the keys it
+// passes over, and what a unit costs beside them (loading and storing its rows:
+// measured at three to four tiles).  Only the balance depends on it.
+constexpr int kUnitCost = 4 * kTile;
+__device__ __forceinline__ int64_t cost_base(const SeqInfo& s) { return max(s.p0, 0) + kUnitCost; }
 __device__ __forceinline__ int64_t cost_flat(const AttParams& p) {
-  return p.window ? static_cast<int64_t>(p.G) * (static_cast<int64_t>(p.window) + p.sinks + 2 * kTile) +
-                        kBlockRows
+  return p.window ? static_cast<int64_t>(p.window) + p.sinks + 2 * p.T + kUnitCost
                   : 0x3fffffffffffffffLL;
 }
 __device__ __forceinline__ int64_t cost_of(const AttParams& p, const SeqInfo& s, int64_t m) {
-  const int64_t c = static_cast<int64_t>(p.G) * (max(s.p0, 0) + kTile) + kBlockRows * (m + 1);
-  return min(c, cost_flat(p));
+  return min(cost_base(s) + 2 * p.T * (m + 1), cost_flat(p));
 }
 __device__ __forceinline__ int64_t cost_before(const AttParams& p, const SeqInfo& s, int64_t m) {
-  const int64_t base = static_cast<int64_t>(p.G) * (max(s.p0, 0) + kTile);
-  const int64_t flat = cost_flat(p);
+  const int64_t base = cost_base(s), flat = cost_flat(p);
   // blocks below `lin` grow with m, those from it on cost `flat`
-  int64_t lin = flat > base ? (flat - base) / kBlockRows : 0;
-  lin = min(lin, m);
-  return lin * base + kBlockRows * (lin * (lin + 1) / 2) + (m - lin) * (m > lin ? flat : 0);
+  int64_t lin = m;
+  if (p.window) lin = min(m, flat > base ? (flat - base) / (2 * p.T) : 0);
+  return lin * base + p.T * (lin * (lin + 1)) + (m > lin ? (m - lin) * flat : 0);
 }
 
 // Tiles of a unit: `sink` tiles from the start, then tiles lo.. .
@@ -109,16 +113,13 @@ struct Tiles {
   int n;     // tiles in all
   int sink;
   int lo;
-  int rows;  // valid rows of the unit
+  int toks;  // tokens of the unit
 };
 
 __device__ __forceinline__ Tiles unit_tiles(const AttParams& p, const SeqInfo& s, int m) {
   Tiles t;
-  const int64_t r0 = static_cast<int64_t>(m) * kBlockRows;
-  const int64_t all = static_cast<int64_t>(s.n) * p.G;
-  t.rows = static_cast<int>(min(static_cast<int64_t>(kBlockRows), all - r0));
-  const int p_first = s.p0 + static_cast<int>(r0 / p.G);
-  const int p_last = s.p0 + static_cast<int>((r0 + t.rows - 1) / p.G);
+  t.toks = min(2 * p.T, s.n - m * 2 * p.T);
+  const int p_first = s.p0 + m * 2 * p.T, p_last = p_first + t.toks - 1;
   const int end = p_last < 0 ? 1 : p_last / kTile + 1;  // a unit that sees nothing passes one tile
   t.lo = 0;
   t.sink = 0;
@@ -129,6 +130,22 @@ __device__ __forceinline__ Tiles unit_tiles(const AttParams& p, const SeqInfo& s
   }
   t.n = t.sink + end - t.lo;
   return t;
+}
+// The tile at which a cost offset falls.  Every CTA and the joining kernel must
+// agree on it, so each operation is rounded on its own; monotone in off.
+__device__ __forceinline__ int tile_of(int64_t off, int64_t cost, int n) {
+  if (off <= 0) return 0;
+  if (off >= cost) return n;
+  const float f = __fdiv_rn(__ll2float_rn(off), __ll2float_rn(cost));
+  return min(n, __float2int_rd(__fmul_rn(f, __int2float_rn(n))));
+}
+// Point c of a line of `total` (< 2^48) cut evenly in n <= p.workers; for n =
+// p.workers a multiplication by w_inv = 2^64 / workers + 1 stands for the division.
+__device__ __forceinline__ int64_t cut(const AttParams& p, int n, int64_t total, int c) {
+  if (n == 1) return c > 0 ? total : 0;
+  const int64_t q =
+      n == p.workers ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(total), p.w_inv)) : total / n;
+  return q * c + static_cast<int>(total - q * n) * c / n;
 }
 
 // ---- small device helpers --------------------------------------------------------
@@ -154,118 +171,130 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
   return *reinterpret_cast<const float2*>(&r);
 }
-// Joins the parts of the unit that worker blockIdx.x (a CTA, or a warp of the row
-// kernel) opened and did not finish:
-//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  parts in worker order.
-// A warp takes a row: its lanes hold the parts' m and l, 32 at a time.  What it
-// finds in head[2 w] and head[2 w + 1] of worker w:
-//   head[2 w]     x: 1 if w has a part of a unit that an earlier worker opened, in
-//                 slot 2 w, y: 1 if that unit ends there
-//   head[2 w + 1] x: 1 if w opens a unit that it does not finish (slot 2 w + 1),
-//                 y: sequence (list form: 0), z: row block (token), w: key head
-constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 8;       // rows of a block at a time
-constexpr int kMaxParts = 520;     // of one unit: 16384 listed tokens by 32, and the ends
+// A unit that worker w (a CTA, or a warp of the row kernel) opens and does not
+// finish is summed in parts: w leaves its part in workspace slot 2 w + 1, the
+// workers after it that have a tile of the unit theirs in slot 2 e.  They write
+//   head[2 w]     x: 1 if w has a part of a unit that an earlier worker opened
+//   head[2 w + 1] x: 1 if w opens such a unit, y: its first token in the packed
+//                 batch, z: tokens, key head << 16, w: the worker that ends it
+// The last worker with a point of the line before `end`:
+__device__ __forceinline__ int last_worker(const AttParams& p, int n, int64_t total, int64_t end) {
+  int e = static_cast<int>(static_cast<float>(end - 1) / static_cast<float>(total) * n);
+  e = min(max(e, 0), n - 1);
+  while (e > 0 && cut(p, n, total, e) >= end) --e;
+  while (e + 1 < n && cut(p, n, total, e + 1) < end) ++e;
+  return e;
+}
 
-template <int D, bool LIST>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttParams p, int workers, int part_rows) {
-  __shared__ int parts[kMaxParts];  // workspace slots of the unit's parts, in order
-  __shared__ int first_end, warp_n[kJoinThreads / 32];
-  const int c = blockIdx.x;
+// Joins the parts of the unit that worker blockIdx.x opened:
+//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  parts in worker order.
+// A warp takes a row.  Latency is what it costs (a few dependent loads), so up to
+// four parts, the usual case, are loaded at once; more go by 32, a lane holding a
+// part's m and l.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinBlocks = 16;  // blocks that share a dense unit's rows
+
+template <int V>
+__device__ __forceinline__ void load_part(const float* src, float (&y)[V]) {
+  if constexpr (V == 4) {
+    const float4 z = *reinterpret_cast<const float4*>(src);
+    y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
+  } else {
+    const float2 z = *reinterpret_cast<const float2*>(src);
+    y[0] = z.x, y[1] = z.y;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttParams p, int part_rows) {
+  const int c = blockIdx.x, lane = lane_id();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel is done
   const int4 open = p.head[2 * c + 1];
   if (!open.x) return;
-  int64_t t0;
-  int rows;
-  if constexpr (LIST) {
-    if (open.z >= p.n_tok) return;
-    const int b = __ldg(p.seq_of + open.z);
-    if (b < 0 || b >= p.n_seq) return;
-    t0 = open.z;
-    rows = p.G;
-  } else {
-    const SeqInfo s = seq_info(p, open.y);
-    const Tiles t = unit_tiles(p, s, open.z);
-    t0 = s.t0;
-    rows = t.rows;
-  }
-  if (static_cast<int>(blockIdx.y) * 8 >= rows) return;
-  // the workers that follow, up to the one that ends the unit (one whose share of
-  // it is less than a tile has no part)
-  int n = 1;
-  if (threadIdx.x == 0) {
-    parts[0] = 2 * c + 1;
-    first_end = workers;
-  }
-  for (int e0 = c + 1; e0 < workers; e0 += kJoinThreads) {
-    const int e = e0 + static_cast<int>(threadIdx.x);
-    const int4 cont = e < workers ? p.head[2 * e] : make_int4(0, 0, 0, 0);
-    __syncthreads();
-    if (cont.y) atomicMin(&first_end, e);
-    __syncthreads();
-    const int end = first_end;
-    const bool mine = cont.x && e <= end;
-    const uint32_t vote = __ballot_sync(0xffffffffu, mine);
-    if (lane_id() == 0) warp_n[warp_id()] = __popc(vote);
-    __syncthreads();
-    int at = n;
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
-      if (w < warp_id()) at += warp_n[w];
-      n += warp_n[w];
-    }
-    at += __popc(vote & ((1u << lane_id()) - 1u));
-    if (mine && at < kMaxParts) parts[at] = 2 * e;
-    if (end < e0 + kJoinThreads) break;
-  }
-  n = min(n, kMaxParts);
-  __syncthreads();
-
+  const int rows = (open.z & 0xffff) * p.G, j = open.z >> 16, n = open.w - c + 1;
+  int x = blockIdx.y * kJoinWarps + warp_id();
+  if (x >= rows) return;
+  bool has[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) has[i] = i == 0 || (i < n && p.head[2 * (c + i)].x);
   constexpr int V = D / 32;  // elements of a lane
-  const int lane = lane_id();
-  for (int r = blockIdx.y * 8 + warp_id(); r < rows; r += gridDim.y * 8) {
-    float m = -INFINITY, l = 0.0f, o[V];
+  for (; x < rows; x += gridDim.y * kJoinWarps) {
+    const int tok = x * p.g_inv >> 16, hd = x - tok * p.G;
+    const int r = tok < p.T ? x : x - p.T * p.G + kTile;  // workspace row: slot 1 starts at 128
+    auto at = [&](int i) {  // row of part i
+      return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * part_rows + r;
+    };
+    float m, l = 0.0f, o[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.0f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float pm = -INFINITY, pl = 0.0f;
-      int64_t q = 0;
-      if (i0 + lane < n) {
-        q = static_cast<int64_t>(parts[i0 + lane]) * part_rows + r;
-        const float2 x = *reinterpret_cast<const float2*>(p.ml + 2 * q);
-        pm = x.x;
-        pl = x.y;
-      }
-      float top = fmaxf(pm, m);
+    for (int e = 0; e < V; ++e) o[e] = 0.0f;
+    if (n <= 4) {
+      float pm[4], pl[4], y[4][V];
 #pragma unroll
-      for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-      const float ref = top == -INFINITY ? 0.0f : top;
-      const float f0 = ex2(m - ref), f = ex2(pm - ref);
-      float lsum = f * pl;
-#pragma unroll
-      for (int s = 16; s > 0; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
-      l = l * f0 + lsum;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o[i] *= f0;
-      m = top;
-      const int left = min(32, n - i0);
-#pragma unroll 4
-      for (int x = 0; x < left; ++x) {
-        const float w = __shfl_sync(0xffffffffu, f, x);
-        const int64_t qx = __shfl_sync(0xffffffffu, q, x);
-        float y[V];
-        if constexpr (V == 4) {
-          const float4 z = *reinterpret_cast<const float4*>(p.po + qx * D + lane * V);
-          y[0] = z.x, y[1] = z.y, y[2] = z.z, y[3] = z.w;
-        } else {
-          const float2 z = *reinterpret_cast<const float2*>(p.po + qx * D + lane * V);
-          y[0] = z.x, y[1] = z.y;
+      for (int i = 0; i < 4; ++i) {
+        pm[i] = -INFINITY;
+        pl[i] = 0.0f;
+        if (has[i]) {
+          const float2 z = *reinterpret_cast<const float2*>(p.ml + 2 * at(i));
+          pm[i] = z.x;
+          pl[i] = z.y;
+          load_part<V>(p.po + at(i) * D + lane * V, y[i]);
         }
+      }
+      m = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+      const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = fmaf(w, y[i], o[i]);
+      for (int i = 0; i < 4; ++i) {
+        if (!has[i]) continue;
+        const float f = ex2(pm[i] - ref);
+        l = fmaf(f, pl[i], l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(f, y[i][e], o[e]);
+      }
+    } else {
+      m = -INFINITY;
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        float pm = -INFINITY, pl = 0.0f;
+        const bool mine = i < n && (i == 0 || p.head[2 * (c + i)].x);
+        if (mine) {
+          const float2 z = *reinterpret_cast<const float2*>(p.ml + 2 * at(i));
+          pm = z.x;
+          pl = z.y;
+        }
+        float top = fmaxf(pm, m);
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        const float f0 = ex2(m - ref), f = ex2(pm - ref);
+        float lsum = f * pl;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
+        l = l * f0 + lsum;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] *= f0;
+        m = top;
+        const uint32_t there = __ballot_sync(0xffffffffu, mine);
+        const int left = min(32, n - i0);
+        for (int s0 = 0; s0 < left; s0 += 8) {  // eight parts' loads in flight
+          float y[8][V], w[8];
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            w[s] = __shfl_sync(0xffffffffu, f, (s0 + s) & 31);
+            const bool in = s0 + s < left && ((there >> (s0 + s)) & 1u);
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[s][e] = 0.0f;
+            if (in) load_part<V>(p.po + at(i0 + s0 + s) * D + lane * V, y[s]);
+            if (!in) w[s] = 0.0f;
+          }
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = fmaf(w[s], y[s][e], o[e]);
+        }
       }
     }
-    const int64_t rr = (LIST ? 0 : static_cast<int64_t>(open.z) * kBlockRows) + r;
-    const int64_t row = (t0 + rr / p.G) * p.H + open.w * p.G + rr % p.G;
+    const int64_t row = static_cast<int64_t>(open.y + tok) * p.H + j * p.G + hd;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint32_t w[V / 2];
 #pragma unroll
@@ -274,8 +303,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttParams p, i
       *reinterpret_cast<uint2*>(p.out + row * D + lane * V) = make_uint2(w[0], w[1]);
     else
       *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V) = w[0];
-    if (p.lse && lane == 0)
-      p.lse[row] = row_lse(m, l);
+    if (p.lse && lane == 0) p.lse[row] = row_lse(m, l);
   }
 }
 
@@ -289,15 +317,15 @@ struct AttWs {
     head = o;  // (of 8 warps a CTA in the row kernel)
     o += (n * 16 * sizeof(int4) + 255) / 256 * 256;
     ml = o;
-    o += n * 2 * kBlockRows * 2 * sizeof(float);
+    o += n * 2 * kPartRows * 2 * sizeof(float);
     po = o;
-    o += n * 2 * kBlockRows * static_cast<size_t>(d) * sizeof(float);
+    o += n * 2 * kPartRows * static_cast<size_t>(d) * sizeof(float);
     total = o;
   }
 };
 
 // The parameters that both kernels read, from the call's description.
-inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl) {
+inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl, int workers) {
   AttParams p{};
   p.Q = a.Q;
   p.kp = a.k_pages;
@@ -319,6 +347,9 @@ inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl) {
   p.H = a.H;
   p.Hkv = a.Hkv;
   p.G = a.H / a.Hkv;
+  p.T = kTile / p.G;
+  p.workers = workers;
+  p.w_inv = workers > 1 ? ~uint64_t{0} / static_cast<uint64_t>(workers) + 1 : 0;
   p.g_inv = 65536 / p.G + 1;
   p.window = a.window;
   p.sinks = a.sinks;
@@ -335,10 +366,10 @@ inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl) {
 
 // The joining kernel, launched while the attention runs (it waits for its end
 // before it reads).
-template <int D, bool LIST>
-cudaError_t launch_join(const AttParams& p, int workers, int part_rows, int y, cudaStream_t s) {
+template <int D>
+cudaError_t launch_join(const AttParams& p, int part_rows, int y, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(workers, y);
+  cfg.gridDim = dim3(p.workers, y);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -346,7 +377,7 @@ cudaError_t launch_join(const AttParams& p, int workers, int part_rows, int y, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, LIST>, p, workers, part_rows);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, part_rows);
 }
 
 }  // namespace

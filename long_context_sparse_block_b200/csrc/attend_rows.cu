@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) list_rows_kernel(const AttPara
   constexpr int E = L::ENTRIES, UPR = D / 8;
   extern __shared__ __align__(128) uint8_t smem_rows[];
   const int lane = lane_id();
-  const int worker = blockIdx.x * kWarps + warp_id();
+  const int worker = warp_id() * gridDim.x + blockIdx.x;  // few workers: one per SM first
   const uint32_t ring = smem_u32(smem_rows) + warp_id() * L::WARP_BYTES;
   volatile uint32_t* masks =
       reinterpret_cast<volatile uint32_t*>(smem_rows + L::OFF_MASK) + warp_id() * L::MASKS;
@@ -91,23 +91,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) list_rows_kernel(const AttPara
   Cursor cur;
   {
     const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * nt;
-    const int64_t n = static_cast<int64_t>(gridDim.x) * kWarps, w = worker;
-    const int64_t x0 = total / n * w + total % n * w / n;
-    const int64_t x1 = total / n * (w + 1) + total % n * (w + 1) / n;
+    const int64_t x0 = cut(p, p.workers, total, min(worker, p.workers));
+    const int64_t x1 = cut(p, p.workers, total, min(worker + 1, p.workers));
     const int64_t unit = x0 / nt;
     cur.t = static_cast<int>(unit / p.Hkv);
     cur.j = static_cast<int>(unit % p.Hkv);
     cur.i = static_cast<int>(x0 % nt);
     cur.left = x1 - x0;
-    if (lane == 0) {
+    if (lane == 0 && worker < p.workers) {
       int4 cont = make_int4(0, 0, 0, 0), open = make_int4(0, 0, 0, 0);
-      if (cur.i > 0 && cur.left > 0) {
-        cont.x = 1;
-        cont.y = cur.left >= nt - cur.i;
-      }
+      cont.x = cur.i > 0 && cur.left > 0;
       const int64_t ue = x1 / nt;
-      if (x1 % nt != 0 && x1 > x0 && ue * nt >= x0)
-        open = make_int4(1, 0, static_cast<int>(ue / p.Hkv), static_cast<int>(ue % p.Hkv));
+      if (x1 % nt != 0 && x1 > x0 && ue * nt >= x0) {
+        const int t = static_cast<int>(ue / p.Hkv);
+        const int b = __ldg(p.seq_of + t);
+        if (b >= 0 && b < p.n_seq)  // (else: left as it was)
+          open = make_int4(1, t, 1 | static_cast<int>(ue - static_cast<int64_t>(t) * p.Hkv) << 16,
+                           last_worker(p, p.workers, total, (ue + 1) * nt));
+      }
       p.head[2 * worker] = cont;
       p.head[2 * worker + 1] = open;
     }
@@ -358,14 +359,21 @@ cudaError_t launch_rows(const AttParams& p, cudaStream_t s) {
   const int n = att_ctas();
   list_rows_kernel<D><<<n, kWarps * 32, L::BYTES, s>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_join<D, true>(p, n * kWarps, kRows, 1, s);
+  if (e != cudaSuccess || p.workers == 1) return e;
+  return launch_join<D>(p, kRows, 1, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_rows(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
-  const AttParams p = att_params(a, ctl);
+  // at least 4 groups a worker: below that a unit falls into so many parts that
+  // joining them costs more than the shorter stretches save (8 rows of 2048 tokens,
+  // 16 heads: 47 us with one group a worker, 18 us with four)
+  const int64_t groups =
+      static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kGroup - 1) / kGroup);
+  const int workers =
+      static_cast<int>(std::min<int64_t>(att_ctas() * kWarps, std::max<int64_t>(1, groups / 4)));
+  const AttParams p = att_params(a, ctl, workers);
   return a.d == 128 ? launch_rows<128>(p, s) : launch_rows<64>(p, s);
 }
 
