@@ -45,13 +45,27 @@ struct RopeParams {
   int offset;
   int tokens;               // tokens per CTA
   int heads;                // heads per CTA
+  int h_inv;                // 65536 / heads + 1: x / heads == x * h_inv >> 16 for x < 256
   float amplitude;
   float sign;               // -1: the transpose
   DevCtl ctl;
 };
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<const float2*>(&r);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -64,9 +78,9 @@ __device__ __forceinline__ uint16_t pack_e4m3(float lo, float hi) {
 }
 
 // D: head size; PAIRED: interleaved layout; F8: e4m3 output; PAGED: rows go to
-// cache slots.  blockIdx.x: group of tokens, y: group of heads, z: 0 the rotated
+// cache slots; SAME: a thread's rows are heads of one token.  blockIdx.x: group of tokens, y: group of heads, z: 0 the rotated
 // rows, 1 the values (copied).
-template <int D, bool PAIRED, bool F8, bool PAGED>
+template <int D, bool PAIRED, bool F8, bool PAGED, bool SAME>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
   constexpr int UPR = D / 8;  // units (lanes) per head row
   extern __shared__ float smem_cs[];  // [tokens][r]: cosines, then sines, of each token
@@ -78,31 +92,47 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const bool values = PAGED && blockIdx.z == 1;
   const uint16_t* src = values ? p.v : p.x;
 
-  // this thread's units, and where they go (-1: nowhere)
+  // this thread's units: kUnits rows one after the other, heads of one token (SAME)
+  // or mostly; and the rows they go to (-1: nowhere)
   uint4 in[kUnits];
   int64_t dst[kUnits];
   int tok[kUnits];
+  auto row_of = [&](int t) -> int64_t {  // row of token t's heads in the result
+    if constexpr (PAGED) {
+      const int64_t slot = __ldg(p.slots + t);
+      if (slot < p.rows_cap) return slot;
+      report(p.ctl, DEV_BAD_INPUT);
+      return -1;
+    }
+    return __ldg(p.positions + t) < 0 ? -1 : t;  // (a row of no sequence: left as it was)
+  };
+  if constexpr (SAME) {
+    const int row = (threadIdx.x / UPR) * kUnits;
+    const int tl = nh == p.heads ? row * p.h_inv >> 16 : 0, h = h0 + row - tl * p.heads;
+    const bool live = row < rows;
+    const int64_t out = live ? row_of(t0 + tl) : -1;
+    const uint4* at = reinterpret_cast<const uint4*>(
+        src + (static_cast<int64_t>(t0 + tl) * p.H + h) * D + u * 8);
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int row = (threadIdx.x / UPR) * kUnits + i;  // heads of one token, mostly
-    dst[i] = -1;
-    tok[i] = 0;
-    in[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows) {
-      const int tl = row / nh, h = h0 + row - tl * nh, t = t0 + tl;
-      tok[i] = tl;
-      in[i] = *reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(t) * p.H + h) * D + u * 8);
-      int64_t out = t;
-      if constexpr (PAGED) {
-        out = __ldg(p.slots + t);
-        if (out >= p.rows_cap) {
-          report(p.ctl, DEV_BAD_INPUT);
-          out = -1;
-        }
-      } else if (__ldg(p.positions + t) < 0) {
-        out = -1;  // a row of no sequence: left as it was
+    for (int i = 0; i < kUnits; ++i) {
+      in[i] = live ? at[i * UPR] : make_uint4(0, 0, 0, 0);
+      dst[i] = out < 0 ? -1 : out * p.H + h + i;
+      tok[i] = min(tl, nt - 1);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int row = (threadIdx.x / UPR) * kUnits + i;
+      const int tl = nh == p.heads ? row * p.h_inv >> 16 : row / nh;
+      dst[i] = -1;
+      tok[i] = min(tl, nt - 1);
+      in[i] = make_uint4(0, 0, 0, 0);
+      if (row < rows) {
+        const int h = h0 + row - tl * nh, t = t0 + tl;
+        in[i] = *reinterpret_cast<const uint4*>(src + (static_cast<int64_t>(t) * p.H + h) * D + u * 8);
+        const int64_t out = row_of(t);
+        if (out >= 0) dst[i] = out * p.H + h;
       }
-      if (out >= 0) dst[i] = out * p.H + h;
     }
   }
   if (values) {
@@ -135,28 +165,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const bool low = u - first < (units >> 1);
   const int other = turned ? lane + (low ? (units >> 1) : -(units >> 1)) : lane;
   const int pi = turned ? (PAIRED ? u - first : u - first - (low ? 0 : (units >> 1))) * NP : 0;
-  float cc[NP], ss[NP];
+  float2 cc[NP / 2], ss[NP / 2];  // cosines, sines (signed for this lane's half)
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    if (i == 0 || tok[i] != tok[i - 1]) {
+    if (i == 0 || (!SAME && tok[i] != tok[i - 1])) {
       const float* cs = smem_cs + tok[i] * p.r + pi;
 #pragma unroll
       for (int j = 0; j < NP; j += 4) {
         const float4 c = *reinterpret_cast<const float4*>(cs + j);
-        const float4 s = *reinterpret_cast<const float4*>(cs + half + j);
-        cc[j] = c.x, cc[j + 1] = c.y, cc[j + 2] = c.z, cc[j + 3] = c.w;
-        ss[j] = s.x, ss[j + 1] = s.y, ss[j + 2] = s.z, ss[j + 3] = s.w;
+        float4 s = *reinterpret_cast<const float4*>(cs + half + j);
+        if (!PAIRED && low) s = make_float4(-s.x, -s.y, -s.z, -s.w);
+        cc[j / 2] = make_float2(c.x, c.y), cc[j / 2 + 1] = make_float2(c.z, c.w);
+        ss[j / 2] = make_float2(s.x, s.y), ss[j / 2 + 1] = make_float2(s.z, s.w);
       }
     }
-    float e[8] = {bf_lo(in[i].x), bf_hi(in[i].x), bf_lo(in[i].y), bf_hi(in[i].y),
-                  bf_lo(in[i].z), bf_hi(in[i].z), bf_lo(in[i].w), bf_hi(in[i].w)};
+    float2 e[4] = {unpack_bf16(in[i].x), unpack_bf16(in[i].y), unpack_bf16(in[i].z), unpack_bf16(in[i].w)};
     if constexpr (PAIRED) {
       if (turned) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float a = e[2 * j], b = e[2 * j + 1];
-          e[2 * j] = a * cc[j] - b * ss[j];
-          e[2 * j + 1] = a * ss[j] + b * cc[j];
+          const float c = j & 1 ? cc[j / 2].y : cc[j / 2].x, s = j & 1 ? ss[j / 2].y : ss[j / 2].x;
+          e[j] = make_float2(e[j].x * c - e[j].y * s, e[j].x * s + e[j].y * c);
         }
       }
     } else {
@@ -165,52 +194,51 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       o.y = __shfl_sync(0xffffffffu, in[i].y, other);
       o.z = __shfl_sync(0xffffffffu, in[i].z, other);
       o.w = __shfl_sync(0xffffffffu, in[i].w, other);
-      if (turned) {
-        const float f[8] = {bf_lo(o.x), bf_hi(o.x), bf_lo(o.y), bf_hi(o.y),
-                            bf_lo(o.z), bf_hi(o.z), bf_lo(o.w), bf_hi(o.w)};
+      if (turned) {  // a cos - b sin, or b cos + a sin
+        const float2 f[4] = {unpack_bf16(o.x), unpack_bf16(o.y), unpack_bf16(o.z), unpack_bf16(o.w)};
 #pragma unroll
-        for (int j = 0; j < 8; ++j)  // a cos - b sin, or b cos + a sin
-          e[j] = e[j] * cc[j] + f[j] * (low ? -ss[j] : ss[j]);
+        for (int j = 0; j < 4; ++j) e[j] = fma2(f[j], ss[j], mul2(e[j], cc[j]));
       }
     }
     if constexpr (F8) {
-      // scale = largest magnitude / 448 (1 for a row of zeros); codes rounded to
-      // nearest even from the 32-bit rotated values times 1 / scale: within 2^-23
-      // of the quotient, so a code differs from the quotient's only next to a tie
-      // (eight divisions a lane took 87 us where one takes 41 on 8192 x 64 x 128)
+      // scale = largest magnitude / 448 (1 for a row of zeros), made by a product
+      // with the rounded 1 / 448 (2^-23); codes rounded to nearest even from the
+      // 32-bit rotated values times an approximate 1 / scale: within 2^-22 of the
+      // quotient, so a code differs from the quotient's only next to a tie.  The
+      // kernel is bound by its instructions: with a division per element it took 87
+      // us on 8192 x 64 x 128, with two per row and scalar products 63, so 45.
       float m = 0.0f;
-      bool bad = false;
+      float2 nz = make_float2(0.0f, 0.0f);  // NaN when an element is not finite
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m = fmaxf(m, fabsf(e[j]));
-        bad = bad || !(fabsf(e[j]) <= 3.402823466e38f);
+      for (int j = 0; j < 4; ++j) {
+        m = fmaxf(fmaxf(m, fabsf(e[j].x)), fabsf(e[j].y));
+        nz = fma2(e[j], make_float2(0.0f, 0.0f), nz);
       }
 #pragma unroll
       for (int o = 1; o < UPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float scale = m / 448.0f;
-      if (scale == 0.0f) scale = 1.0f;  // a row of zeros, or too small to have a scale
+      float scale = m * (1.0f / 448.0f), inv = rcp_approx(scale);
+      if (m < 1e-30f) {  // zero, or a scale next to the subnormals
+        scale = m / 448.0f;
+        if (scale == 0.0f) scale = 1.0f;
+        inv = fminf(1.0f / scale, 3.402823466e38f);
+      }
       if (dst[i] >= 0) {
-        if (bad) report(p.ctl, DEV_BAD_INPUT);
-        uint2 w;
-        const float inv = fminf(1.0f / scale, 3.402823466e38f);  // (finite for the smallest scales)
-        const uint32_t q0 = pack_e4m3(e[0] * inv, e[1] * inv);
-        const uint32_t q1 = pack_e4m3(e[2] * inv, e[3] * inv);
-        const uint32_t q2 = pack_e4m3(e[4] * inv, e[5] * inv);
-        const uint32_t q3 = pack_e4m3(e[6] * inv, e[7] * inv);
-        w.x = q0 | (q1 << 16);
-        w.y = q2 | (q3 << 16);
-        *reinterpret_cast<uint2*>(p.y8 + dst[i] * D + u * 8) = w;
+        if (!(nz.x + nz.y == 0.0f)) report(p.ctl, DEV_BAD_INPUT);
+        const float2 iv = make_float2(inv, inv);
+        uint32_t w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 x = mul2(e[2 * j], iv), y = mul2(e[2 * j + 1], iv);
+          w[j] = pack_e4m3(x.x, x.y) | static_cast<uint32_t>(pack_e4m3(y.x, y.y)) << 16;
+        }
+        *reinterpret_cast<uint2*>(p.y8 + dst[i] * D + u * 8) = make_uint2(w[0], w[1]);
         if (u == 0) p.scale[dst[i]] = scale;
       }
     } else {
-      if (dst[i] >= 0) {
-        uint4 w;
-        w.x = pack_bf16(e[0], e[1]);
-        w.y = pack_bf16(e[2], e[3]);
-        w.z = pack_bf16(e[4], e[5]);
-        w.w = pack_bf16(e[6], e[7]);
-        *reinterpret_cast<uint4*>(p.y + dst[i] * D + u * 8) = w;
-      }
+      if (dst[i] >= 0)
+        *reinterpret_cast<uint4*>(p.y + dst[i] * D + u * 8) =
+            make_uint4(pack_bf16(e[0].x, e[0].y), pack_bf16(e[1].x, e[1].y),
+                       pack_bf16(e[2].x, e[2].y), pack_bf16(e[3].x, e[3].y));
     }
   }
 }
@@ -221,10 +249,15 @@ cudaError_t launch_one(RopeParams p, cudaStream_t s) {
   constexpr int ROWS = kUnits * kRopeThreads / (D / 8);
   p.heads = p.H < ROWS ? p.H : ROWS;
   p.tokens = ROWS / p.heads;
+  p.h_inv = 65536 / p.heads + 1;
   const int smem = p.tokens * p.r * static_cast<int>(sizeof(float));
   static_assert(ROWS * D * 4 <= 48 * 1024, "a row's cosines and sines per row of the CTA");
   const dim3 grid((p.n + p.tokens - 1) / p.tokens, (p.H + p.heads - 1) / p.heads, p.v ? 2 : 1);
-  rope_kernel<D, PAIRED, F8, PAGED><<<grid, kRopeThreads, smem, s>>>(p);
+  // heads in whole fours (and the last group of a larger H too): one token a thread
+  if (p.H % kUnits == 0)
+    rope_kernel<D, PAIRED, F8, PAGED, true><<<grid, kRopeThreads, smem, s>>>(p);
+  else
+    rope_kernel<D, PAIRED, F8, PAGED, false><<<grid, kRopeThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
