@@ -1,0 +1,190 @@
+"""A serving session: one attention layer with the MISA indexer in front of it, over
+paged caches that live on the device.
+
+    plan -> append (rotate, quantise, write) -> pool -> route -> score + top-k
+         -> attention over the selected tokens (or over everything, dense)
+
+Every sequence has a row of one block table; index keys, keys and values lie in three
+page pools under the same page ids.  A step adds new tokens to any of the sequences:
+`begin` plans it (pages, slots, positions, lengths: one launch), `append` writes the
+rotated rows, and `decode` (one new token for each sequence), `prefill` (a chunk of
+one sequence) or `dense` (any mixture, without the indexer) give the attention's
+results.  Buffers are allocated once; the calls only launch the library's kernels on
+the current stream.  The host keeps the lengths too (it gives the new tokens of each
+step), so that a step that does not fit is refused before anything is launched.
+"""
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+
+
+@dataclass
+class SessionShape:
+    n_seq: int              # rows of the block table
+    max_len: int            # most tokens of a sequence
+    n_pages: int            # pages of the pools
+    page_size: int          # 16, 32, 64 or 128
+    H: int                  # index heads
+    d: int                  # index head size
+    B: int                  # pooling block
+    h: int                  # routed index heads
+    k: int                  # selected tokens
+    Hq: int                 # query heads of the attention
+    Hkv: int                # key heads
+    dh: int                 # attention head size (64 or 128)
+    rope_dim: int           # rotated elements of an attention head, from rope_offset on
+    rope_offset: int = 0
+    index_rope_dim: int = 0     # rotated elements of an index head (0: rope_dim)
+    interleaved: bool = False
+    rope_base: float = 10000.0
+    rope_scaling: str = "plain"
+    rope_factor: float = 1.0
+    trained_len: float = 4096.0
+    fp8_index: bool = False     # index keys as e4m3 codes with a scale per token
+
+    @property
+    def max_blocks(self) -> int:
+        return -(-self.max_len // self.page_size)
+
+    @property
+    def M_max(self) -> int:
+        return -(-self.max_blocks * self.page_size // self.B)
+
+
+class MisaSession:
+    def __init__(self, shape: SessionShape, device="cuda"):
+        s = self.shape = shape
+        dev = self.device = torch.device(device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        self.tables = torch.zeros((s.n_seq, s.max_blocks), **i32)
+        self.lens = torch.zeros(s.n_seq, **i32)
+        self.free_pages = torch.arange(s.n_pages - 1, -1, -1, **i32)
+        self.free_count = torch.full((1,), s.n_pages, **i32)
+        index = (s.n_pages, s.page_size, s.d)
+        self.index_pages = (torch.zeros(index, dtype=torch.uint8, device=dev) if s.fp8_index
+                            else torch.zeros(index, **bf))
+        self.index_scale = (torch.ones(index[:2], dtype=torch.float32, device=dev) if s.fp8_index
+                            else None)
+        kv = (s.n_pages, s.page_size, s.Hkv, s.dh)
+        self.k_pages, self.v_pages = torch.zeros(kv, **bf), torch.zeros(kv, **bf)
+        self.kbar_hl = torch.zeros((s.n_seq, 2, s.M_max, s.d), dtype=torch.int16, device=dev)
+        self.ws = torch.empty(_lib.misa_workspace_size("attend", 1, 0, s.dh, 0), dtype=torch.uint8,
+                              device=dev)
+
+        def freqs(dim):
+            return _lib.misa_rope_frequencies(dim, s.rope_base, s.rope_scaling, s.rope_factor,
+                                              s.trained_len, device=dev)
+        self.inv_freq, self.amplitude = freqs(s.rope_dim)
+        self.index_freq, _ = freqs(s.index_rope_dim or s.rope_dim)
+        self._len = [0] * s.n_seq
+        self._free = s.n_pages
+        self.plan = None
+
+    def _pages(self, n: int) -> int:
+        return -(-n // self.shape.page_size)
+
+    def begin(self, q_lens, n_tok: int | None = None) -> _lib.StepPlan:
+        """Plans a step that adds q_lens[b] (host integers) new tokens to each sequence;
+        n_tok >= sum(q_lens) rows of the packed batch (rows past the sum are padding)."""
+        s = self.shape
+        q = [int(x) for x in q_lens]
+        if len(q) != s.n_seq or min(q, default=0) < 0:
+            raise ValueError(f"q_lens: one count >= 0 for each of {s.n_seq} sequences")
+        new = [a + b for a, b in zip(self._len, q)]
+        if max(new, default=0) > s.max_len:
+            raise ValueError(f"a sequence would pass max_len = {s.max_len} tokens")
+        need = sum(self._pages(a) - self._pages(b) for a, b in zip(new, self._len))
+        if need > self._free:
+            raise ValueError(f"the step needs {need} pages, {self._free} are free")
+        total = sum(q)
+        if n_tok is None:
+            n_tok = total
+        if n_tok < total:
+            raise ValueError(f"n_tok = {n_tok} rows cannot hold {total} new tokens")
+        qd = torch.tensor(q, dtype=torch.int32).to(self.device)
+        self.plan = _lib.misa_plan_step(qd, self.lens, self.tables, s.page_size, n_tok=n_tok,
+                                        n_pages=s.n_pages, free_pages=self.free_pages,
+                                        free_count=self.free_count, seq_lens=self.lens)
+        self._len, self._free, self._q = new, self._free - need, q
+        return self.plan
+
+    def release(self, seqs) -> None:
+        """Ends sequences: their pages go back to the pool, their lengths become 0."""
+        flags = [0] * self.shape.n_seq
+        for b in seqs:
+            flags[b] = 1
+        _lib.misa_release_pages(torch.tensor(flags, dtype=torch.int32).to(self.device), self.lens,
+                                self.tables, self.shape.page_size, self.free_pages, self.free_count,
+                                n_pages=self.shape.n_pages)
+        for b, f in enumerate(flags):
+            if f:
+                self._free += self._pages(self._len[b])
+                self._len[b] = 0
+
+    def append(self, index_k, k, v) -> None:
+        """Rotates the step's rows and writes them into the caches: index_k [n_tok, d], k and v
+        [n_tok, Hkv, dh] bf16 (v is not rotated)."""
+        s, p = self.shape, self.plan
+        _lib.misa_cache_append(index_k, p.positions, p.slots, self.index_freq, self.index_pages,
+                               k_scale=self.index_scale, interleaved=s.interleaved,
+                               amplitude=self.amplitude)
+        _lib.misa_cache_append(k, p.positions, p.slots, self.inv_freq, self.k_pages, v=v,
+                               v_pages=self.v_pages, offset=s.rope_offset, interleaved=s.interleaved,
+                               amplitude=self.amplitude)
+
+    def rotate(self, q, index_q=None):
+        """The step's query rows [n_tok, Hq, dh] (and index queries [n_tok, H, d]) rotated."""
+        s, p = self.shape, self.plan
+        q = _lib.misa_rope(q, p.positions, self.inv_freq, offset=s.rope_offset,
+                           interleaved=s.interleaved, amplitude=self.amplitude)
+        if index_q is None:
+            return q
+        return q, _lib.misa_rope(index_q, p.positions, self.index_freq, interleaved=s.interleaved,
+                                 amplitude=self.amplitude)
+
+    def dense(self, q, window: int = 0, sinks: int = 0, want_lse: bool = False):
+        """Attention of the step's rotated queries over everything they see."""
+        p = self.plan
+        return _lib.misa_attend_paged(q, self.k_pages, self.v_pages, self.tables, p.cu_q, p.seq_lens,
+                                      window=window, sinks=sinks, want_lse=want_lse, ws=self.ws)
+
+    def decode(self, q, index_q, w, want_lse: bool = False):
+        """One new token for each sequence (begin([1] * n_seq)): the indexer's selection over each
+        sequence's keys and the attention over it -> (out, lse or None, idx [n_seq, k]).
+        q, index_q rotated, w [n_seq, H] fp32."""
+        s, p = self.shape, self.plan
+        if self._q != [1] * s.n_seq or p.positions.numel() != s.n_seq:
+            raise ValueError("decode takes a step of one new token for each sequence")
+        # blocks of the new token only; a sequence that just came out of a prefill was
+        # pooled there
+        _lib.misa_decode_pool_keys(self.index_pages, self.tables, p.seq_lens, s.B, s.M_max, 1,
+                                   kbar_hl=self.kbar_hl, k_scale=self.index_scale)
+        heads, _ = _lib.misa_decode_route_heads(index_q, w, self.kbar_hl, p.seq_lens, s.B, s.h)
+        idx, _ = _lib.misa_decode_score_topk(index_q, w, heads, self.index_pages, self.tables,
+                                             p.seq_lens, s.k, k_scale=self.index_scale)
+        out, lse = _lib.misa_attend_selected(q, self.k_pages, self.v_pages, self.tables, p.seq_of,
+                                             p.positions, idx, want_lse=want_lse, ws=self.ws)
+        return out, lse, idx
+
+    def prefill(self, b: int, q, index_q, w, want_lse: bool = False):
+        """The step's chunk of sequence b, the only one with new tokens: selection and attention
+        -> (out, lse or None, idx [n, k]).  q, index_q rotated, w [n, H] fp32."""
+        s, p = self.shape, self.plan
+        n, n_k = self._q[b], self._len[b]
+        if n == 0 or sum(self._q) != n or p.positions.numel() != n:
+            raise ValueError(f"prefill takes a step whose new tokens are all of sequence {b}")
+        keys = _lib.PagedKeys(self.index_pages, self.tables[b], n_k, k_scale=self.index_scale)
+        M = -(-n_k // s.B)
+        hl = torch.empty((2, M, s.d), dtype=torch.int16, device=self.device)
+        _lib.misa_pool_keys(keys, s.B, kbar_hl=hl, want_kbar=False)
+        self.kbar_hl[b, :, :M] = hl          # what decode goes on from
+        heads, _ = _lib.misa_route_heads(index_q, w, hl, n_k - n, n_k, s.B, s.h)
+        idx = _lib.misa_score_topk(index_q, w, heads, keys, n_k - n, s.k)
+        out, lse = _lib.misa_attend_selected(q, self.k_pages, self.v_pages, self.tables, p.seq_of,
+                                             p.positions, idx, want_lse=want_lse, ws=self.ws)
+        return out, lse, idx

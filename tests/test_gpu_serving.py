@@ -1,0 +1,178 @@
+"""A serving session from end to end: prefill of two sequences, decode steps, a release,
+against the same steps made one by one on contiguous keys (the indexer's selection, bit
+for bit) and against attention in 64 bits over what was selected."""
+import numpy as np
+import pytest
+import torch
+
+from tests.serving_helpers import attention_row, rotated
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from long_context_sparse_block_b200 import _lib
+    return _lib
+
+
+def _session(fp8, dh=128, Hkv=2):
+    from long_context_sparse_block_b200.serving import MisaSession, SessionShape
+    return MisaSession(SessionShape(
+        n_seq=3, max_len=700, n_pages=40, page_size=32, H=16, d=64, B=32, h=4, k=48, Hq=8, Hkv=Hkv,
+        dh=dh, rope_dim=32, rope_offset=dh - 32, interleaved=True, rope_scaling="bands",
+        rope_factor=4.0, trained_len=256.0, fp8_index=fp8))
+
+
+def _rows(n, s, seed):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *sh: torch.randn(sh, generator=g).to(torch.bfloat16).cuda()
+    return dict(index_k=r(n, s.d), k=r(n, s.Hkv, s.dh), v=r(n, s.Hkv, s.dh), q=2 * r(n, s.Hq, s.dh),
+                index_q=r(n, s.H, s.d), w=r(n, s.H).float())
+
+
+def _check_out(ses, out, lse, q, idx, b, pos):
+    """Every row over its own selection, from the caches as they are."""
+    s = ses.shape
+    for t in range(out.shape[0]):
+        sel = idx[t][idx[t] >= 0].long().cpu()
+        assert int(sel.max()) <= pos[t] and sel.unique().numel() == sel.numel() == min(s.k, pos[t] + 1)
+        seq = b[t]
+        table = ses.tables[seq].cpu().long()
+        phys = table[sel // s.page_size] * s.page_size + sel % s.page_size
+        K = ses.k_pages.view(-1, s.Hkv, s.dh)[phys.cuda()].double().cpu()
+        V = ses.v_pages.view(-1, s.Hkv, s.dh)[phys.cuda()].double().cpu()
+        for h in range(s.Hq):
+            o, l, tol, tl = attention_row(q[t, h].double().cpu(), K[:, h // (s.Hq // s.Hkv)],
+                                          V[:, h // (s.Hq // s.Hkv)], s.dh ** -0.5)
+            assert ((out[t, h].double().cpu() - o).abs() <= tol).all(), (t, h)
+            assert abs(float(lse[t, h]) - l) <= tl, (t, h)
+
+
+@pytest.mark.parametrize("fp8,dh,Hkv", [(False, 128, 2), (True, 64, 1)])
+def test_prefill_decode_and_release(lib, fp8, dh, Hkv):
+    ses = _session(fp8, dh, Hkv)
+    s = ses.shape
+    index = {}
+    # prefill sequence 0 in two chunks and sequence 2 in one
+    for b, n, seed in ((0, 300, 1), (2, 97, 2), (0, 131, 3)):
+        before = ses._len[b]
+        ses.begin([n if x == b else 0 for x in range(3)])
+        r = _rows(n, s, seed)
+        ses.append(r["index_k"], r["k"], r["v"])
+        index.setdefault(b, []).append(r["index_k"])
+        q, iq = ses.rotate(r["q"], r["index_q"])
+        out, lse, idx = ses.prefill(b, q, iq, r["w"], want_lse=True)
+        assert lib.misa_last_device_status() == lib.MISA_OK
+        # the same selection from contiguous rotated keys
+        n_k = before + n
+        pos = torch.arange(n_k, dtype=torch.int32, device="cuda")
+        keys = torch.cat(index[b]).view(n_k, 1, s.d)
+        kw = dict(interleaved=True, amplitude=ses.amplitude)
+        if fp8:
+            K, ks = lib.misa_rope_fp8(keys, pos, ses.index_freq, **kw)
+            K, ks = K.view(n_k, s.d), ks.view(n_k)
+        else:
+            K, ks = lib.misa_rope(keys, pos, ses.index_freq, **kw).view(n_k, s.d), None
+        _, hl = lib.misa_pool_keys(K, s.B, k_scale=ks)
+        heads, _ = lib.misa_route_heads(iq, r["w"], hl, before, n_k, s.B, s.h)
+        want = lib.misa_score_topk(iq, r["w"], heads, K, before, s.k, k_scale=ks)
+        assert torch.equal(idx, want)
+        rows = [0, 1, n // 2, n - 1]
+        _check_out(ses, out[rows], lse[rows], q[rows], idx[rows], [b] * 4, [before + t for t in rows])
+        # the queries' rotation against the formula
+        pr = np.arange(before, n_k)
+        yq, mag = rotated(r["q"].float().cpu().numpy(), pr, ses.inv_freq.cpu().numpy(), s.rope_offset,
+                          True, ses.amplitude)
+        assert np.all(np.abs(q.double().cpu().numpy() - yq) <= 2.0 ** -21 * mag + 2.0 ** -8 * np.abs(yq))
+        # everything instead of a selection
+        full, flse = ses.dense(q, want_lse=True)
+        table = ses.tables[b].cpu().long()
+        for t in rows:
+            sel = torch.arange(before + t + 1)
+            phys = (table[sel // s.page_size] * s.page_size + sel % s.page_size).cuda()
+            Kc = ses.k_pages.view(-1, s.Hkv, s.dh)[phys].double().cpu()
+            Vc = ses.v_pages.view(-1, s.Hkv, s.dh)[phys].double().cpu()
+            o, l, tol, tl = attention_row(q[t, 3].double().cpu(), Kc[:, 3 // (s.Hq // Hkv)],
+                                          Vc[:, 3 // (s.Hq // Hkv)], s.dh ** -0.5)
+            assert ((full[t, 3].double().cpu() - o).abs() <= tol).all()
+            assert abs(float(flse[t, 3]) - l) <= tl
+    # decode: sequence 1 starts from nothing
+    for i in range(3):
+        ses.begin([1, 1, 1])
+        r = _rows(3, s, 10 + i)
+        ses.append(r["index_k"], r["k"], r["v"])
+        q, iq = ses.rotate(r["q"], r["index_q"])
+        out, lse, idx = ses.decode(q, iq, r["w"], want_lse=True)
+        assert lib.misa_last_device_status() == lib.MISA_OK
+        _check_out(ses, out, lse, q, idx, [0, 1, 2], [x - 1 for x in ses._len])
+        for b in range(3):                        # the pooled keys are those of the whole cache
+            n_k = ses._len[b]
+            keys = lib.PagedKeys(ses.index_pages, ses.tables[b], n_k, k_scale=ses.index_scale)
+            _, hl = lib.misa_pool_keys(keys, s.B)
+            assert torch.equal(ses.kbar_hl[b, :, :hl.shape[1]], hl)
+    assert ses.lens.tolist() == ses._len == [434, 3, 100]
+    free = ses._free
+    ses.release([0])
+    assert ses._len == [0, 3, 100] and int(ses.free_count) == ses._free == free + 14
+    assert sorted(ses.free_pages.tolist()[:ses._free]) == sorted(
+        set(range(s.n_pages)) - set(ses.tables[1].tolist()[:1]) - set(ses.tables[2].tolist()[:4]))
+
+
+def test_padded_steps_leave_the_rest_alone(lib):
+    ses = _session(False)
+    s = ses.shape
+    plan = ses.begin([3, 0, 2], n_tok=9)
+    r = _rows(9, s, 5)
+    ses.append(r["index_k"], r["k"], r["v"])
+    assert plan.slots.tolist()[5:] == [-1] * 4
+    used = {int(x) for x in plan.slots.tolist()[:5]}
+    rows = ses.k_pages.view(-1, s.Hkv * s.dh)
+    touched = {int(x) for x in torch.nonzero(rows.abs().sum(-1)).flatten()}
+    assert touched == used
+    q = ses.rotate(r["q"])
+    out, _ = ses.dense(q)
+    assert out.shape[0] == 9 and not torch.isnan(out[:5]).any()
+    with pytest.raises(ValueError, match="pages"):
+        ses.begin([600, 600, 600])
+    with pytest.raises(ValueError, match="max_len"):
+        ses.begin([800, 0, 0])
+    with pytest.raises(ValueError):
+        ses.decode(q, r["index_q"], r["w"])
+
+
+def test_a_captured_decode_step(lib):
+    # one decode step in a graph: each replay appends a token to every sequence
+    ses = _session(False)
+    s = ses.shape
+    for b in range(3):
+        n = 40 + 30 * b
+        ses.begin([n if x == b else 0 for x in range(3)])
+        r = _rows(n, s, 20 + b)
+        ses.append(r["index_k"], r["k"], r["v"])
+        ses.prefill(b, *ses.rotate(r["q"], r["index_q"]), r["w"])
+    r = _rows(3, s, 30)
+    one = torch.ones(3, dtype=torch.int32, device="cuda")
+    def step():
+        p = ses.plan = lib.misa_plan_step(one, ses.lens, ses.tables, s.page_size, n_tok=3,
+                                          n_pages=s.n_pages, free_pages=ses.free_pages,
+                                          free_count=ses.free_count, seq_lens=ses.lens)
+        ses._q = [1, 1, 1]
+        ses.append(r["index_k"], r["k"], r["v"])
+        q, iq = ses.rotate(r["q"], r["index_q"])
+        return ses.decode(q, iq, r["w"], want_lse=True) + (q, p)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse, idx, q, p = step()
+    for i in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert lib.misa_last_device_status() == lib.MISA_OK
+        lens = [42 + i, 72 + i, 102 + i]
+        assert ses.lens.tolist() == lens and p.positions.tolist() == [x - 1 for x in lens]
+        _check_out(ses, out, lse, q, idx, [0, 1, 2], [x - 1 for x in lens])
