@@ -721,6 +721,9 @@ def misa_cache_append(k, positions, slots, inv_freq, k_pages, k_scale=None, v=No
     _check("misa_cache_append", st)
 
 
+_ATTEND_WS = {}  # workspace bytes by (device, head size): they depend on nothing else
+
+
 def _attend_args(Q, k_pages, v_pages, block_tables, scale, out, want_lse, lse, ws):
     """What the two attention calls share, checked: addresses, sizes, results, workspace."""
     if Q.dim() != 3 or k_pages.dim() != 4 or block_tables.dim() != 2:
@@ -743,9 +746,11 @@ def _attend_args(Q, k_pages, v_pages, block_tables, scale, out, want_lse, lse, w
     results = (_arg(out, n_tok * H * d, _BF16_CODES, "out", dev),
                None if lse is None else _arg(lse, n_tok * H, _F32, "lse", dev))
     stream = _raw_stream(dev)
-    ws_bytes = _lib.misa_workspace_size(b"attend", 1, 0, d, 0)
+    ws_bytes = _ATTEND_WS.get((dev, d))
+    if ws_bytes is None:
+        ws_bytes = _ATTEND_WS[dev, d] = _lib.misa_workspace_size(b"attend", 1, 0, d, 0)
     if ws is None:
-        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=Q.device)
+        ws = Q.new_empty((ws_bytes,), dtype=torch.uint8)
     elif ws.numel() * ws.element_size() < ws_bytes:
         raise ValueError(f"ws holds {ws.numel() * ws.element_size()} bytes, the call needs {ws_bytes}")
     work = (_arg(ws, 0, (ws.dtype,), "ws", dev), ws.numel() * ws.element_size(), stream)

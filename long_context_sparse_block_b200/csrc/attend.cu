@@ -69,266 +69,10 @@ struct AttLayout {
   static_assert(ALLOC <= 232448, "shared memory of an SM");
 };
 
-// What the roles work on: tiles [i0, i1) of a unit, whole or a part.  Written to
-// shared memory by the scheduling warp, a few ahead.
-struct __align__(16) Seg {
-  int valid;   // 0: the end
-  int len;     // keys of the sequence
-  int p0;      // position of the unit's first token
-  int pad0;
-  int b, m, j;
-  int i0, i1;
-  int part;    // workspace slot, or -1: the whole unit
-  int split;   // both slots share the rows (alternate tiles)
-  int toks;    // tokens of the unit
-  int tb;      // its first token in the packed batch
-  int sink, lo;
-  int pad;
-  __device__ __forceinline__ int key0(int i) const { return (i < sink ? i : lo + i - sink) * kTile; }
-  // tiles of a slot
-  __device__ __forceinline__ int tiles_of(int slot) const {
-    const int n = i1 - i0;
-    return split ? (n + 1 - slot) >> 1 : n;
-  }
-};
-static_assert(sizeof(Seg) == 64, "segment slot");
-
-// Where the CTA's stretch of the line begins and how long it is.
-struct Start {
-  Unit u;
-  int64_t left;
-  int64_t x1, total;  // its end on the line, and the line's
-  int workers;        // CTAs that share it
-};
-
-template <bool LIST>
-struct Walk {
-  Unit u;
-  int64_t left;
-  int cta;
-  __device__ __forceinline__ void init(const Start& st, int c) {
-    u = st.u;
-    left = st.left;
-    cta = c;
-  }
-  // The next non-empty segment; valid = 0 at the end of the stretch.
-  __device__ __forceinline__ void next(const AttParams& p, Seg& g) {
-    g.valid = 0;
-    while (left > 0) {
-      if constexpr (LIST) {
-        if (u.m >= p.n_tok) return;
-        const int nt = (p.k + kTile - 1) / kTile;
-        g.i0 = static_cast<int>(u.off);
-        g.i1 = static_cast<int>(min(static_cast<int64_t>(nt), u.off + left));
-        g.b = __ldg(p.seq_of + u.m);
-        g.m = u.m;
-        g.j = u.j;
-        left -= g.i1 - g.i0;
-        u.off = 0;
-        if (++u.j == p.Hkv) {
-          u.j = 0;
-          ++u.m;
-        }
-        if (g.b < 0) continue;  // a row of no sequence: left as it was
-        if (g.b >= p.n_seq) {
-          report(p.ctl, DEV_BAD_INPUT);
-          continue;
-        }
-        g.tb = g.m;
-        g.p0 = __ldg(p.positions + g.m);
-        g.len = 0;
-        g.toks = 1;
-        g.sink = g.lo = 0;
-        g.split = 1;
-        g.part = g.i0 > 0 ? 2 * cta : g.i1 < nt ? 2 * cta + 1 : -1;
-        g.valid = 1;
-        return;
-      } else {
-        if (u.b >= p.n_seq) return;
-        const SeqInfo s = seq_info(p, u.b);
-        if (s.n == 0) {
-          ++u.b;
-          continue;
-        }
-        const Tiles t = unit_tiles(p, s, u.m);
-        const int64_t cost = cost_of(p, s, u.m);
-        const int64_t end = min(cost, u.off + left);
-        g.i0 = tile_of(u.off, cost, t.n);
-        g.i1 = tile_of(end, cost, t.n);
-        g.b = u.b;
-        g.m = u.m;
-        g.j = u.j;
-        left -= end - u.off;
-        u.off = 0;
-        if (++u.j == p.Hkv) {
-          u.j = 0;
-          if (++u.m >= row_blocks(p, s)) {
-            u.m = 0;
-            ++u.b;
-          }
-        }
-        if (g.i1 <= g.i0) continue;
-        g.tb = static_cast<int>(s.t0) + g.m * 2 * p.T;
-        g.len = s.len;
-        g.p0 = s.p0 + g.m * 2 * p.T;
-        g.toks = t.toks;
-        g.sink = t.sink;
-        g.lo = t.lo;
-        g.split = t.toks <= p.T;
-        g.part = g.i0 > 0 ? 2 * cta : g.i1 < t.n ? 2 * cta + 1 : -1;
-        g.valid = 1;
-        return;
-      }
-    }
-  }
-};
-
-// The unit at point x of a sequence's costs.
-__device__ __forceinline__ Unit locate(const AttParams& p, const SeqInfo& s, int b, int64_t x) {
-  int64_t lo = 0, hi = row_blocks(p, s) - 1;
-  while (lo < hi) {  // the last block that starts at or before x
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (cost_before(p, s, mid) * p.Hkv <= x)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  x -= cost_before(p, s, lo) * p.Hkv;
-  const int64_t c = cost_of(p, s, lo);
-  int j = 0;
-  for (; x >= c; ++j) x -= c;
-  return Unit{b, static_cast<int>(lo), j, x};
-}
-
-struct PlanShared {
-  Unit at[2];       // the units at the two ends of the stretch
-  int64_t warp_sum[16];
-};
-
-// Finds the CTA's stretch of the line, cut(total, c) to cut(total, c + 1):
-// a block scan of the sequences' costs, again for the units when the threads do
-// not hold all sequences.
-template <int THREADS>
-__device__ __forceinline__ void plan_stretch(const AttParams& p, PlanShared& ps, Start& st) {
-  const int tid = threadIdx.x;
-  if (tid < 2) ps.at[tid] = Unit{p.n_seq, 0, 0, 0};
-  int64_t total = 0, x0 = 0, x1 = 0;
-  SeqInfo s{};
-  int64_t cost = 0, first = 0;
-  // cost and first point of sequence base + tid; total grows by the chunk's costs
-  auto scan = [&](int base) {
-    const int b = base + tid;
-    cost = 0;
-    if (b < p.n_seq) {
-      s = seq_info(p, b);
-      if (s.n > 0) cost = cost_before(p, s, row_blocks(p, s)) * p.Hkv;
-    }
-    int64_t x = cost;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane_id() >= o) x += y;
-    }
-    __syncthreads();
-    if (lane_id() == 31) ps.warp_sum[warp_id()] = x;
-    __syncthreads();
-    first = total + x - cost;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-      const int64_t v = ps.warp_sum[w];
-      if (w < warp_id()) first += v;
-      total += v;
-    }
-  };
-  auto find = [&](int base) {
-    if (x0 >= first && x0 < first + cost) ps.at[0] = locate(p, s, base + tid, x0 - first);
-    if (x1 >= first && x1 < first + cost) ps.at[1] = locate(p, s, base + tid, x1 - first);
-  };
-  for (int base = 0; base < p.n_seq; base += THREADS) {
-    scan(base);
-    const int b = base + tid;
-    if (blockIdx.x == 0 && b < p.n_seq) {
-      const int len = __ldg(p.lens + b);
-      if (len < 0 || len > (static_cast<int64_t>(p.max_blocks) << p.page_shift))
-        report(p.ctl, DEV_BAD_INPUT);
-    }
-  }
-  const int64_t all = total;
-  // a stretch is worth two tiles at least: shorter ones only add parts to join
-  st.workers = static_cast<int>(min(static_cast<int64_t>(p.workers), max(all >> 8, int64_t{1})));
-  const int c = min(static_cast<int>(blockIdx.x), st.workers);
-  x0 = cut(p, st.workers, all, c);
-  x1 = cut(p, st.workers, all, min(c + 1, st.workers));
-  if (p.n_seq <= THREADS) {
-    find(0);
-  } else {
-    total = 0;
-    for (int base = 0; base < p.n_seq; base += THREADS) {
-      scan(base);
-      find(base);
-    }
-  }
-  __syncthreads();
-  st.u = ps.at[0];
-  st.left = x1 - x0;
-  st.x1 = x1;
-  st.total = all;
-}
-
-// Tile boundary of a unit at cost offset `off`.
-__device__ __forceinline__ int tile_at(const AttParams& p, const Unit& u, int& n) {
-  const SeqInfo s = seq_info(p, u.b);
-  n = unit_tiles(p, s, u.m).n;
-  return tile_of(u.off, cost_of(p, s, u.m), n);
-}
-
 // List form: with 8 units or more for a CTA, units are left whole (the CTAs' work
 // then differs by one unit at most) and nothing has to be joined.
 __host__ __device__ inline bool whole_units(const AttParams& p, int ctas) {
   return static_cast<int64_t>(p.n_tok) * p.Hkv >= 8ll * ctas;
-}
-
-// What the CTA will leave in the workspace, for the joining kernel.
-template <bool LIST>
-__device__ __forceinline__ void write_head(const AttParams& p, const Start& st, const Unit& end) {
-  const int c = blockIdx.x;
-  int4 cont = make_int4(0, 0, 0, 0), open = make_int4(0, 0, 0, 0);
-  const int nl = (p.k + kTile - 1) / kTile;
-  const bool same = st.u.b == end.b && st.u.m == end.m && st.u.j == end.j;
-  auto past = [&](const Unit& u) { return LIST ? u.m >= p.n_tok : u.b >= p.n_seq; };
-  auto tile = [&](const Unit& u, int& n) {
-    if (!LIST) return tile_at(p, u, n);
-    n = nl;
-    return static_cast<int>(u.off);
-  };
-  int i0 = 0, n = 0;
-  if (!past(st.u)) i0 = tile(st.u, n);
-  if (i0 > 0) {
-    int n2;
-    cont.x = (same ? tile(end, n2) : n) > i0;
-  }
-  if (st.left > 0 && !past(end) && end.off > 0 && !(same && i0 > 0)) {
-    int n2;
-    const int e = tile(end, n2);
-    if (e > 0 && e < n2) {  // (e == n2: whole)
-      int tok = end.m, toks = 1;
-      int64_t cost = nl;
-      bool there = true;
-      if constexpr (LIST) {
-        const int b = __ldg(p.seq_of + end.m);
-        there = b >= 0 && b < p.n_seq;  // (else: left as it was)
-      } else {
-        const SeqInfo s = seq_info(p, end.b);
-        tok = static_cast<int>(s.t0) + end.m * 2 * p.T;
-        toks = unit_tiles(p, s, end.m).toks;
-        cost = cost_of(p, s, end.m);
-      }
-      if (there)
-        open = make_int4(1, tok, toks | end.j << 16, last_worker(p, st.workers, st.total, st.x1 - end.off + cost));
-    }
-  }
-  p.head[2 * c] = cont;
-  p.head[2 * c + 1] = open;
 }
 
 // The low n bits (n clamped to 0..32).
@@ -407,7 +151,7 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
   constexpr int ST = L::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
-  PlanShared& ps = *reinterpret_cast<PlanShared*>(smem);  // before the query rows arrive
+  auto& ps = *reinterpret_cast<PlanShared<2>*>(smem);  // before the query rows arrive
   const uint32_t sQ = smem_u32(smem + L::OFF_Q);
   const uint32_t sKV = smem_u32(smem + L::OFF_KV);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
@@ -459,28 +203,11 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
     tmem_relinquish();
   }
   Start st;
-  Unit end;  // the unit in which the next CTA's stretch begins
   if constexpr (LIST) {
-    // every unit costs its tiles: the stretch is a division away
-    const int nt = (p.k + kTile - 1) / kTile;
-    const int64_t step = whole_units(p, p.workers) ? nt : 1;
-    const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * (nt / step);
-    const int64_t x0 = cut(p, p.workers, total, blockIdx.x) * step;
-    const int64_t x1 = cut(p, p.workers, total, blockIdx.x + 1) * step;
-    auto unit = [&](int64_t x) {
-      const int64_t q = x / nt;
-      const int t = static_cast<int>(q / p.Hkv);
-      return Unit{0, t, static_cast<int>(q - static_cast<int64_t>(t) * p.Hkv), x - q * nt};
-    };
-    st.u = unit(x0);
-    st.left = x1 - x0;
-    st.x1 = x1;
-    st.total = total * step;
-    st.workers = p.workers;
-    end = unit(x1);
+    st = list_start(p, blockIdx.x, whole_units(p, p.workers) ? list_tiles(p) : 1);
   } else {
-    plan_stretch<L::THREADS>(p, ps, st);
-    end = ps.at[1];
+    plan_points<L::THREADS>(p, ps, [&](int i) { return static_cast<int>(blockIdx.x) + i; });
+    st = plan_start(ps, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -513,7 +240,7 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         const int32_t* bt = p.bts + static_cast<int64_t>(g.b) * p.max_blocks;
         auto page_row = [&](int x) -> int {  // this lane's page of tile x
           if (lane >= per || x >= n) return 0;
-          const int64_t s0 = static_cast<int64_t>(g.key0(g.i0 + x)) + lane * page;
+          const int64_t s0 = static_cast<int64_t>(g.key0(g.i0 + x, 7)) + lane * page;
           int64_t y = p.key_rows;  // past the sequence: a box of fill rows
           if (s0 < g.len) {
             int64_t pg = __ldg(bt + (s0 >> p.page_shift));
@@ -580,7 +307,7 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
       const Seg& gs = seg_at(sg);
       const int n = __shfl_sync(0xffffffffu, gs.i1 - gs.i0, 0);
       const bool split = __shfl_sync(0xffffffffu, gs.split, 0) != 0;
-      const int key0 = gs.key0(gs.i1 - 1);
+      const int key0 = gs.key0(gs.i1 - 1, 7);
       const bool tail =
           __shfl_sync(0xffffffffu, !LIST && gs.len > key0 && gs.len < key0 + kTile, 0) != 0;
       __syncwarp();
@@ -709,7 +436,7 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
         walk.next(p, g);
         segs[sg % kSegs] = g;
         mbar_arrive(bar(GFULL + sg % kSegs));
-        if (sg == 0) write_head<LIST>(p, st, end);
+        if (sg == 0) write_head<LIST>(p, st, blockIdx.x);
         if (!g.valid) break;
       }
     }
@@ -737,7 +464,7 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
                         g.tb + i * p.T);
       }
       __syncwarp();
-      const int key0 = g.key0(g.i1 - 1);
+      const int key0 = g.key0(g.i1 - 1, 7);
       if (!LIST && g.len > key0 && g.len < key0 + kTile) {
         // the last tile's value rows past the end of the sequence
         const uint32_t e = ring + 2 * n - 1, stage = e % ST;  // the segment's last entry
@@ -796,7 +523,7 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
             w[q] = __ballot_sync(0xffffffffu, s >= 0 && s <= pos && s < cap);
           }
         } else {
-          const int key0 = g.key0(x);
+          const int key0 = g.key0(x, 7);
           const int lim = pos - key0 + 1;  // keys of the tile at or before the query
 #pragma unroll
           for (int q = 0; q < 4; ++q) w[q] = low_bits(lim - 32 * q);
@@ -1097,11 +824,14 @@ cudaError_t launch_att(const AttParams& p, const CUtensorMap& qm, const CUtensor
 size_t attend_workspace(int d) { return AttWs(d).total; }
 
 cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
+  // at most 16 rows a unit, on average: a warp each (see attend_rows.cu)
+  const int G = a.H / a.Hkv;
+  if (G <= kRowHeads && (a.idx || static_cast<int64_t>(a.n_tok) * G <= static_cast<int64_t>(kRowHeads) * a.n_seq))
+    return launch_attend_rows(a, ctl, s);
   const int64_t tiles = a.idx ? static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kTile - 1) / kTile)
                               : att_ctas();
   const AttParams p =
-      att_params(a, ctl, static_cast<int>(std::min<int64_t>(att_ctas(), tiles)));
-  if (a.idx && p.G <= kRowHeads) return launch_attend_rows(a, ctl, s);
+      att_params(a, ctl, static_cast<int>(std::min<int64_t>(att_ctas(), tiles)), false);
   CUtensorMap qm, km, vm;
   std::memset(&km, 0, sizeof km);
   std::memset(&vm, 0, sizeof vm);

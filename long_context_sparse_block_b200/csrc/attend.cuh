@@ -14,7 +14,7 @@ constexpr int kTile = 128;       // keys per tile of the dense form
 constexpr int kPartRows = 256;   // workspace rows of a part (two slots of 128)
 constexpr float kRaise = 8.0f;   // log2 of the largest weight before m is raised
 constexpr int kMaxCtas = 256;
-constexpr int kRowHeads = 16;    // list form: query heads of a key head that the row kernel takes
+constexpr int kRowHeads = 16;    // rows of a unit of the row kernel
 
 struct AttParams {
   const uint16_t* Q;        // [n_tok, H, D]
@@ -37,7 +37,11 @@ struct AttParams {
   int H;
   int Hkv;
   int G;
-  int T;                    // tokens of a slot: 128 / G
+  int T;                    // tokens of a slot of rows: 128 / G (row kernel: 16 / G)
+  int TU;                   // tokens of a unit: two slots (row kernel: one)
+  int tile_sh;              // log2 of a tile's keys: 7 (row kernel: 5)
+  int unit_cost;            // what a unit costs beside its keys, in keys
+  int least_sh;             // log2 of the keys that a worker's stretch is worth at least
   int g_inv;                // 65536 / G + 1: x / G == x * g_inv >> 16 for x < 384, G <= 128
   int window;               // 0: none
   int sinks;
@@ -83,29 +87,30 @@ __device__ __forceinline__ SeqInfo seq_info(const AttParams& p, int b) {
   return s;
 }
 
-// A unit's rows are the G heads of 2 T tokens: two slots of T tokens, head by head.
+// A unit's rows are the G heads of TU tokens, in slots of T tokens.
 __device__ __forceinline__ int64_t row_blocks(const AttParams& p, const SeqInfo& s) {
-  return (static_cast<int64_t>(s.n) + 2 * p.T - 1) / (2 * p.T);
+  return (static_cast<int64_t>(s.n) + p.TU - 1) / p.TU;
 }
 
 // Cost of block m of a sequence and its sum over blocks 0..m-1: about the keys it
 // passes over, and what a unit costs beside them (loading and storing its rows:
-// measured at three to four tiles).  Only the balance depends on it.
-constexpr int kUnitCost = 4 * kTile;
-__device__ __forceinline__ int64_t cost_base(const SeqInfo& s) { return max(s.p0, 0) + kUnitCost; }
+// measured at three to four tiles of 128).  Only the balance depends on it.
+__device__ __forceinline__ int64_t cost_base(const AttParams& p, const SeqInfo& s) {
+  return max(s.p0, 0) + p.unit_cost;
+}
 __device__ __forceinline__ int64_t cost_flat(const AttParams& p) {
-  return p.window ? static_cast<int64_t>(p.window) + p.sinks + 2 * p.T + kUnitCost
+  return p.window ? static_cast<int64_t>(p.window) + p.sinks + p.TU + p.unit_cost
                   : 0x3fffffffffffffffLL;
 }
 __device__ __forceinline__ int64_t cost_of(const AttParams& p, const SeqInfo& s, int64_t m) {
-  return min(cost_base(s) + 2 * p.T * (m + 1), cost_flat(p));
+  return min(cost_base(p, s) + p.TU * (m + 1), cost_flat(p));
 }
 __device__ __forceinline__ int64_t cost_before(const AttParams& p, const SeqInfo& s, int64_t m) {
-  const int64_t base = cost_base(s), flat = cost_flat(p);
+  const int64_t base = cost_base(p, s), flat = cost_flat(p);
   // blocks below `lin` grow with m, those from it on cost `flat`
   int64_t lin = m;
-  if (p.window) lin = min(m, flat > base ? (flat - base) / (2 * p.T) : 0);
-  return lin * base + p.T * (lin * (lin + 1)) + (m > lin ? (m - lin) * flat : 0);
+  if (p.window) lin = min(m, flat > base ? (flat - base) / p.TU : 0);
+  return lin * base + p.TU * (lin * (lin + 1) / 2) + (m > lin ? (m - lin) * flat : 0);
 }
 
 // Tiles of a unit: `sink` tiles from the start, then tiles lo.. .
@@ -118,15 +123,16 @@ struct Tiles {
 
 __device__ __forceinline__ Tiles unit_tiles(const AttParams& p, const SeqInfo& s, int m) {
   Tiles t;
-  t.toks = min(2 * p.T, s.n - m * 2 * p.T);
-  const int p_first = s.p0 + m * 2 * p.T, p_last = p_first + t.toks - 1;
-  const int end = p_last < 0 ? 1 : p_last / kTile + 1;  // a unit that sees nothing passes one tile
+  t.toks = min(p.TU, s.n - m * p.TU);
+  const int p_first = s.p0 + m * p.TU, p_last = p_first + t.toks - 1;
+  const int end = p_last < 0 ? 1 : (p_last >> p.tile_sh) + 1;  // (one that sees nothing: one tile)
   t.lo = 0;
   t.sink = 0;
   if (p.window) {
     const int64_t f = static_cast<int64_t>(p_first) - p.window + 1;
-    t.lo = f > 0 ? static_cast<int>(f / kTile) : 0;
-    t.sink = min((p.sinks + kTile - 1) / kTile, t.lo);
+    t.lo = f > 0 ? static_cast<int>(f >> p.tile_sh) : 0;
+    const int64_t sinks = (static_cast<int64_t>(p.sinks) + (1 << p.tile_sh) - 1) >> p.tile_sh;
+    t.sink = static_cast<int>(min(sinks, static_cast<int64_t>(t.lo)));
   }
   t.n = t.sink + end - t.lo;
   return t;
@@ -146,6 +152,266 @@ __device__ __forceinline__ int64_t cut(const AttParams& p, int n, int64_t total,
   const int64_t q =
       n == p.workers ? static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(total), p.w_inv)) : total / n;
   return q * c + static_cast<int>(total - q * n) * c / n;
+}
+
+// Tiles of the list form's units.
+__device__ __forceinline__ int list_tiles(const AttParams& p) {
+  return (p.k + (1 << p.tile_sh) - 1) >> p.tile_sh;
+}
+
+// What the roles work on: tiles [i0, i1) of a unit, whole or a part.  Written to
+// shared memory by the scheduling warp, a few ahead.
+struct __align__(16) Seg {
+  int valid;   // 0: the end
+  int len;     // keys of the sequence
+  int p0;      // position of the unit's first token
+  int pad0;
+  int b, m, j;
+  int i0, i1;
+  int part;    // workspace slot, or -1: the whole unit
+  int split;   // both slots share the rows (alternate tiles)
+  int toks;    // tokens of the unit
+  int tb;      // its first token in the packed batch
+  int sink, lo;
+  int pad;
+  // first key of tile i, tiles of 2^sh keys
+  __device__ __forceinline__ int key0(int i, int sh) const { return (i < sink ? i : lo + i - sink) << sh; }
+  // tiles of a slot
+  __device__ __forceinline__ int tiles_of(int slot) const {
+    const int n = i1 - i0;
+    return split ? (n + 1 - slot) >> 1 : n;
+  }
+};
+static_assert(sizeof(Seg) == 64, "segment slot");
+
+// Where a worker's stretch of the line begins, the unit in which the next one's
+// begins, and how long it is.
+struct Start {
+  Unit u, end;
+  int64_t left;
+  int64_t x1, total;  // its end on the line, and the line's
+  int workers;        // that share the line
+};
+
+template <bool LIST>
+struct Walk {
+  Unit u;
+  int64_t left;
+  int worker;
+  __device__ __forceinline__ void init(const Start& st, int w) {
+    u = st.u;
+    left = st.left;
+    worker = w;
+  }
+  // The next non-empty segment; valid = 0 at the end of the stretch.
+  __device__ __forceinline__ void next(const AttParams& p, Seg& g) {
+    g.valid = 0;
+    while (left > 0) {
+      if constexpr (LIST) {
+        if (u.m >= p.n_tok) return;
+        const int nt = list_tiles(p);
+        g.i0 = static_cast<int>(u.off);
+        g.i1 = static_cast<int>(min(static_cast<int64_t>(nt), u.off + left));
+        g.b = __ldg(p.seq_of + u.m);
+        g.m = u.m;
+        g.j = u.j;
+        left -= g.i1 - g.i0;
+        u.off = 0;
+        if (++u.j == p.Hkv) {
+          u.j = 0;
+          ++u.m;
+        }
+        if (g.b < 0) continue;  // a row of no sequence: left as it was
+        if (g.b >= p.n_seq) {
+          report(p.ctl, DEV_BAD_INPUT);
+          continue;
+        }
+        g.tb = g.m;
+        g.p0 = __ldg(p.positions + g.m);
+        g.len = 0;
+        g.toks = 1;
+        g.sink = g.lo = 0;
+        g.split = 1;
+        g.part = g.i0 > 0 ? 2 * worker : g.i1 < nt ? 2 * worker + 1 : -1;
+        g.valid = 1;
+        return;
+      } else {
+        if (u.b >= p.n_seq) return;
+        const SeqInfo s = seq_info(p, u.b);
+        if (s.n == 0) {
+          ++u.b;
+          continue;
+        }
+        const Tiles t = unit_tiles(p, s, u.m);
+        const int64_t cost = cost_of(p, s, u.m);
+        const int64_t end = min(cost, u.off + left);
+        g.i0 = tile_of(u.off, cost, t.n);
+        g.i1 = tile_of(end, cost, t.n);
+        g.b = u.b;
+        g.m = u.m;
+        g.j = u.j;
+        left -= end - u.off;
+        u.off = 0;
+        if (++u.j == p.Hkv) {
+          u.j = 0;
+          if (++u.m >= row_blocks(p, s)) {
+            u.m = 0;
+            ++u.b;
+          }
+        }
+        if (g.i1 <= g.i0) continue;
+        g.tb = static_cast<int>(s.t0) + g.m * p.TU;
+        g.len = s.len;
+        g.p0 = s.p0 + g.m * p.TU;
+        g.toks = t.toks;
+        g.sink = t.sink;
+        g.lo = t.lo;
+        g.split = t.toks <= p.T;
+        g.part = g.i0 > 0 ? 2 * worker : g.i1 < t.n ? 2 * worker + 1 : -1;
+        g.valid = 1;
+        return;
+      }
+    }
+  }
+};
+
+// The unit at point x of a sequence's costs.
+__device__ __forceinline__ Unit locate(const AttParams& p, const SeqInfo& s, int b, int64_t x) {
+  int64_t lo = 0, hi = row_blocks(p, s) - 1;
+  while (lo < hi) {  // the last block that starts at or before x
+    const int64_t mid = (lo + hi + 1) >> 1;
+    if (cost_before(p, s, mid) * p.Hkv <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  x -= cost_before(p, s, lo) * p.Hkv;
+  const int64_t c = cost_of(p, s, lo);
+  int j = 0;
+  for (; x >= c; ++j) x -= c;
+  return Unit{b, static_cast<int>(lo), j, x};
+}
+
+// Points of the line that a CTA looks for: NP, the i-th at cut number index(i).
+template <int NP>
+struct PlanShared {
+  Unit at[NP];
+  int64_t x[NP];
+  int64_t warp_sum[16];
+  int64_t total;
+  int workers;
+};
+
+// Scans the sequences' costs (a block scan, again for the units when the threads do
+// not hold all sequences) and finds the units at the points index(0..NP-1) of the
+// line's cut; ps keeps them and the points.
+template <int THREADS, int NP, typename F>
+__device__ __forceinline__ void plan_points(const AttParams& p, PlanShared<NP>& ps, F&& index) {
+  const int tid = threadIdx.x;
+  if (tid < NP) ps.at[tid] = Unit{p.n_seq, 0, 0, 0};
+  int64_t total = 0;
+  SeqInfo s{};
+  int64_t cost = 0, first = 0;
+  // cost and first point of sequence base + tid; total grows by the chunk's costs
+  auto scan = [&](int base) {
+    const int b = base + tid;
+    cost = 0;
+    if (b < p.n_seq) {
+      s = seq_info(p, b);
+      if (s.n > 0) cost = cost_before(p, s, row_blocks(p, s)) * p.Hkv;
+    }
+    int64_t x = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane_id() >= o) x += y;
+    }
+    __syncthreads();
+    if (lane_id() == 31) ps.warp_sum[warp_id()] = x;
+    __syncthreads();
+    first = total + x - cost;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      const int64_t v = ps.warp_sum[w];
+      if (w < warp_id()) first += v;
+      total += v;
+    }
+  };
+  auto find = [&](int base) {
+    if (cost == 0) return;
+    for (int i = 0; i < NP; ++i) {
+      const int64_t x = ps.x[i] - first;
+      if (x >= 0 && x < cost) ps.at[i] = locate(p, s, base + tid, x);
+    }
+  };
+  for (int base = 0; base < p.n_seq; base += THREADS) {
+    scan(base);
+    const int b = base + tid;
+    if (blockIdx.x == 0 && b < p.n_seq) {
+      const int len = __ldg(p.lens + b);
+      if (len < 0 || len > (static_cast<int64_t>(p.max_blocks) << p.page_shift))
+        report(p.ctl, DEV_BAD_INPUT);
+    }
+  }
+  const int64_t all = total;
+  const int workers =
+      static_cast<int>(min(static_cast<int64_t>(p.workers), max(all >> p.least_sh, int64_t{1})));
+  if (tid < NP) ps.x[tid] = cut(p, workers, all, min(index(tid), workers));
+  if (tid == 0) {
+    ps.total = all;
+    ps.workers = workers;
+  }
+  __syncthreads();
+  if (p.n_seq <= THREADS) {
+    find(0);
+  } else {
+    total = 0;
+    for (int base = 0; base < p.n_seq; base += THREADS) {
+      scan(base);
+      find(base);
+    }
+  }
+  __syncthreads();
+}
+// The stretch between points i and i + 1 of the plan.
+template <int NP>
+__device__ __forceinline__ Start plan_start(const PlanShared<NP>& ps, int i) {
+  Start st;
+  st.u = ps.at[i];
+  st.end = ps.at[i + 1];
+  st.left = ps.x[i + 1] - ps.x[i];
+  st.x1 = ps.x[i + 1];
+  st.total = ps.total;
+  st.workers = ps.workers;
+  return st;
+}
+// The same for the list form, where every unit costs its tiles; step: units are
+// left whole (tiles of a unit) or not (1).
+__device__ __forceinline__ Start list_start(const AttParams& p, int worker, int step) {
+  const int nt = list_tiles(p);
+  const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * (nt / step);
+  const int64_t x0 = cut(p, p.workers, total, min(worker, p.workers)) * step;
+  const int64_t x1 = cut(p, p.workers, total, min(worker + 1, p.workers)) * step;
+  auto unit = [&](int64_t x) {
+    const int64_t q = x / nt;
+    const int t = static_cast<int>(q / p.Hkv);
+    return Unit{0, t, static_cast<int>(q - static_cast<int64_t>(t) * p.Hkv), x - q * nt};
+  };
+  Start st;
+  st.u = unit(x0);
+  st.end = unit(x1);
+  st.left = x1 - x0;
+  st.x1 = x1;
+  st.total = total * step;
+  st.workers = p.workers;
+  return st;
+}
+
+// Tile boundary of a unit at cost offset `off`.
+__device__ __forceinline__ int tile_at(const AttParams& p, const Unit& u, int& n) {
+  const SeqInfo s = seq_info(p, u.b);
+  n = unit_tiles(p, s, u.m).n;
+  return tile_of(u.off, cost_of(p, s, u.m), n);
 }
 
 // ---- small device helpers --------------------------------------------------------
@@ -186,11 +452,55 @@ __device__ __forceinline__ int last_worker(const AttParams& p, int n, int64_t to
   return e;
 }
 
+// What worker c will leave in the workspace, for the joining kernel.
+template <bool LIST>
+__device__ __forceinline__ void write_head(const AttParams& p, const Start& st, int c) {
+  const Unit& end = st.end;
+  int4 cont = make_int4(0, 0, 0, 0), open = make_int4(0, 0, 0, 0);
+  const int nl = list_tiles(p);
+  const bool same = st.u.b == end.b && st.u.m == end.m && st.u.j == end.j;
+  auto past = [&](const Unit& u) { return LIST ? u.m >= p.n_tok : u.b >= p.n_seq; };
+  auto tile = [&](const Unit& u, int& n) {
+    if (!LIST) return tile_at(p, u, n);
+    n = nl;
+    return static_cast<int>(u.off);
+  };
+  int i0 = 0, n = 0;
+  if (!past(st.u)) i0 = tile(st.u, n);
+  if (i0 > 0) {
+    int n2;
+    cont.x = (same ? tile(end, n2) : n) > i0;
+  }
+  if (st.left > 0 && !past(end) && end.off > 0 && !(same && i0 > 0)) {
+    int n2;
+    const int e = tile(end, n2);
+    if (e > 0 && e < n2) {  // (e == n2: whole)
+      int tok = end.m, toks = 1;
+      int64_t cost = nl;
+      bool there = true;
+      if constexpr (LIST) {
+        const int b = __ldg(p.seq_of + end.m);
+        there = b >= 0 && b < p.n_seq;  // (else: left as it was)
+      } else {
+        const SeqInfo s = seq_info(p, end.b);
+        tok = static_cast<int>(s.t0) + end.m * p.TU;
+        toks = unit_tiles(p, s, end.m).toks;
+        cost = cost_of(p, s, end.m);
+      }
+      if (there)
+        open = make_int4(1, tok, toks | end.j << 16, last_worker(p, st.workers, st.total, st.x1 - end.off + cost));
+    }
+  }
+  p.head[2 * c] = cont;
+  p.head[2 * c + 1] = open;
+}
+
 // Joins the parts of the unit that worker blockIdx.x opened:
-//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,  parts in worker order.
-// A warp takes a row.  Latency is what it costs (a few dependent loads), so up to
-// four parts, the usual case, are loaded at once; more go by 32, a lane holding a
-// part's m and l.
+//   o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i
+// in a fixed order.  Latency is what it costs (a few dependent loads).  Up to four
+// parts, the usual case: a warp takes a row and loads them all at once.  More: the
+// block takes a row, warp w the parts w, w + 8, .., eight of them in flight, and the
+// warps' sums meet in shared memory.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinBlocks = 16;  // blocks that share a dense unit's rows
@@ -208,93 +518,22 @@ __device__ __forceinline__ void load_part(const float* src, float (&y)[V]) {
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttParams p, int part_rows) {
-  const int c = blockIdx.x, lane = lane_id();
+  constexpr int V = D / 32;  // elements of a lane
+  __shared__ float meet[kJoinWarps][D + 2];
+  const int c = blockIdx.x, lane = lane_id(), warp = warp_id();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel is done
   const int4 open = p.head[2 * c + 1];
   if (!open.x) return;
   const int rows = (open.z & 0xffff) * p.G, j = open.z >> 16, n = open.w - c + 1;
-  int x = blockIdx.y * kJoinWarps + warp_id();
-  if (x >= rows) return;
-  bool has[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) has[i] = i == 0 || (i < n && p.head[2 * (c + i)].x);
-  constexpr int V = D / 32;  // elements of a lane
-  for (; x < rows; x += gridDim.y * kJoinWarps) {
-    const int tok = x * p.g_inv >> 16, hd = x - tok * p.G;
-    const int r = tok < p.T ? x : x - p.T * p.G + kTile;  // workspace row: slot 1 starts at 128
-    auto at = [&](int i) {  // row of part i
-      return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * part_rows + r;
-    };
-    float m, l = 0.0f, o[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = 0.0f;
-    if (n <= 4) {
-      float pm[4], pl[4], y[4][V];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        pm[i] = -INFINITY;
-        pl[i] = 0.0f;
-        if (has[i]) {
-          const float2 z = *reinterpret_cast<const float2*>(p.ml + 2 * at(i));
-          pm[i] = z.x;
-          pl[i] = z.y;
-          load_part<V>(p.po + at(i) * D + lane * V, y[i]);
-        }
-      }
-      m = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-      const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!has[i]) continue;
-        const float f = ex2(pm[i] - ref);
-        l = fmaf(f, pl[i], l);
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf(f, y[i][e], o[e]);
-      }
-    } else {
-      m = -INFINITY;
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        float pm = -INFINITY, pl = 0.0f;
-        const bool mine = i < n && (i == 0 || p.head[2 * (c + i)].x);
-        if (mine) {
-          const float2 z = *reinterpret_cast<const float2*>(p.ml + 2 * at(i));
-          pm = z.x;
-          pl = z.y;
-        }
-        float top = fmaxf(pm, m);
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        const float ref = top == -INFINITY ? 0.0f : top;
-        const float f0 = ex2(m - ref), f = ex2(pm - ref);
-        float lsum = f * pl;
-#pragma unroll
-        for (int s = 16; s > 0; s >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, s);
-        l = l * f0 + lsum;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] *= f0;
-        m = top;
-        const uint32_t there = __ballot_sync(0xffffffffu, mine);
-        const int left = min(32, n - i0);
-        for (int s0 = 0; s0 < left; s0 += 8) {  // eight parts' loads in flight
-          float y[8][V], w[8];
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            w[s] = __shfl_sync(0xffffffffu, f, (s0 + s) & 31);
-            const bool in = s0 + s < left && ((there >> (s0 + s)) & 1u);
-#pragma unroll
-            for (int e = 0; e < V; ++e) y[s][e] = 0.0f;
-            if (in) load_part<V>(p.po + at(i0 + s0 + s) * D + lane * V, y[s]);
-            if (!in) w[s] = 0.0f;
-          }
-#pragma unroll
-          for (int s = 0; s < 8; ++s)
-#pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = fmaf(w[s], y[s][e], o[e]);
-        }
-      }
-    }
-    const int64_t row = static_cast<int64_t>(open.y + tok) * p.H + j * p.G + hd;
+  auto row_of = [&](int x, int& tok) {  // workspace row of row x: slot 1 starts at 128
+    tok = x * p.g_inv >> 16;
+    return tok < p.T ? x : x - p.T * p.G + kTile;
+  };
+  auto at = [&](int i, int r) {  // row r of part i
+    return static_cast<int64_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * part_rows + r;
+  };
+  auto result = [&](int x, int tok, float m, float l, const float (&o)[V]) {
+    const int64_t row = static_cast<int64_t>(open.y + tok) * p.H + j * p.G + x - tok * p.G;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     uint32_t w[V / 2];
 #pragma unroll
@@ -304,6 +543,107 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const AttParams p, i
     else
       *reinterpret_cast<uint32_t*>(p.out + row * D + lane * V) = w[0];
     if (p.lse && lane == 0) p.lse[row] = row_lse(m, l);
+  };
+
+  if (n <= 4) {
+    bool has[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) has[i] = i == 0 || (i < n && p.head[2 * (c + i)].x);
+    for (int x = blockIdx.y * kJoinWarps + warp; x < rows; x += gridDim.y * kJoinWarps) {
+      int tok;
+      const int r = row_of(x, tok);
+      float m, l = 0.0f, o[V], pm[4], pl[4], y[4][V];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pm[i] = -INFINITY;
+        pl[i] = 0.0f;
+        if (has[i]) {
+          const float2 z = *reinterpret_cast<const float2*>(p.ml + 2 * at(i, r));
+          pm[i] = z.x;
+          pl[i] = z.y;
+          load_part<V>(p.po + at(i, r) * D + lane * V, y[i]);
+        }
+      }
+      m = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+      const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!has[i]) continue;
+        const float f = ex2(pm[i] - ref);
+        l = fmaf(f, pl[i], l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(f, y[i][e], o[e]);
+      }
+      result(x, tok, m, l, o);
+    }
+    return;
+  }
+  for (int x = blockIdx.y; x < rows; x += gridDim.y) {
+    int tok;
+    const int r = row_of(x, tok);
+    float m = -INFINITY, l = 0.0f, o[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] = 0.0f;
+    for (int i0 = warp; i0 < n; i0 += 8 * kJoinWarps) {
+      float pm[8], pl[8], y[8][V];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int i = i0 + s * kJoinWarps;
+        pm[s] = -INFINITY;
+        pl[s] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) y[s][e] = 0.0f;
+        // (a worker whose share of the unit is less than a tile has no part)
+        if (i < n && (i == 0 || p.head[2 * (c + i)].x)) {
+          const float2 z = *reinterpret_cast<const float2*>(p.ml + 2 * at(i, r));
+          pm[s] = z.x;
+          pl[s] = z.y;
+          load_part<V>(p.po + at(i, r) * D + lane * V, y[s]);
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) top = fmaxf(top, pm[s]);
+      const float ref = top == -INFINITY ? 0.0f : top;
+      const float f0 = ex2(m - ref);
+      m = top;
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] *= f0;
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float f = ex2(pm[s] - ref);
+        l = fmaf(f, pl[s], l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(f, y[s][e], o[e]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) meet[warp][lane * V + e] = o[e];
+    if (lane == 0) {
+      meet[warp][D] = m;
+      meet[warp][D + 1] = l;
+    }
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) m = fmaxf(m, meet[w][D]);
+      const float ref = m == -INFINITY ? 0.0f : m;
+      l = 0.0f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = ex2(meet[w][D] - ref);
+        l = fmaf(f, meet[w][D + 1], l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = fmaf(f, meet[w][lane * V + e], o[e]);
+      }
+      result(x, tok, m, l, o);
+    }
+    __syncthreads();
   }
 }
 
@@ -325,7 +665,7 @@ struct AttWs {
 };
 
 // The parameters that both kernels read, from the call's description.
-inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl, int workers) {
+inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl, int workers, bool rows) {
   AttParams p{};
   p.Q = a.Q;
   p.kp = a.k_pages;
@@ -347,7 +687,11 @@ inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl, int worker
   p.H = a.H;
   p.Hkv = a.Hkv;
   p.G = a.H / a.Hkv;
-  p.T = kTile / p.G;
+  p.T = (rows ? kRowHeads : kTile) / p.G;
+  p.TU = rows ? p.T : 2 * p.T;
+  p.tile_sh = rows ? 5 : 7;
+  p.unit_cost = rows ? 128 : 4 * kTile;
+  p.least_sh = rows ? 7 : 8;
   p.workers = workers;
   p.w_inv = workers > 1 ? ~uint64_t{0} / static_cast<uint64_t>(workers) + 1 : 0;
   p.g_inv = 65536 / p.G + 1;
@@ -382,7 +726,8 @@ cudaError_t launch_join(const AttParams& p, int part_rows, int y, cudaStream_t s
 
 }  // namespace
 
-// The list form for few heads per key head (attend_rows.cu).
+// Few rows per key head: the list form, and the dense form of short steps
+// (attend_rows.cu).
 cudaError_t launch_attend_rows(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s);
 
 }  // namespace misa

@@ -24,16 +24,24 @@ namespace misa {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kGroup = 32;  // tokens of a ring entry
-constexpr int kRows = 16;
+constexpr int kGroup = 32;  // tokens summed at a time
 
-template <int D>
+// Ring entries hold 32 tokens' rows in the list form, whose rows come from L2 and
+// which is bound by its instructions (256 rows against 320 us with 16 tokens an entry
+// on 512 rows of 1024 tokens, 8 groups of 8 heads), and 16 in the dense form, which
+// streams from HBM and wants its bytes in flight (5/6 of the ring instead of 2/3:
+// 64 sequences of up to 32768 keys 709 against 781 us).
+template <int D, bool LIST>
 struct RowLayout {
-  static constexpr int ENTRY = kGroup * D * 2;
-  static constexpr int ENTRIES = D == 128 ? 3 : 6;
+  static constexpr int PARTS = LIST ? 1 : 2;  // entries of a group's keys
+  static constexpr int TOKENS = kGroup / PARTS;
+  static constexpr int ENTRY = TOKENS * D * 2;
+  static constexpr int ENTRIES = (D == 128 ? 3 : 6) * PARTS;
   static constexpr int MASKS = 8;  // words of visible tokens, by group
   static constexpr int WARP_BYTES = ENTRIES * ENTRY;
-  static constexpr int OFF_MASK = kWarps * WARP_BYTES;
+  static constexpr int SEGS = 8;   // segments met ahead of the sums
+  static constexpr int OFF_SEG = kWarps * WARP_BYTES;
+  static constexpr int OFF_MASK = OFF_SEG + kWarps * SEGS * static_cast<int>(sizeof(Seg));
   static constexpr int BYTES = OFF_MASK + kWarps * MASKS * 4;
 };
 
@@ -59,206 +67,240 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// A stretch of the line of groups: token t, key head j, group i of nt, `left` more.
-struct Cursor {
-  int t, j, i;
-  int64_t left;
-  __device__ __forceinline__ void step(const AttParams& p, int nt) {
-    --left;
-    if (++i == nt) {
-      i = 0;
-      if (++j == p.Hkv) {
-        j = 0;
-        ++t;
-      }
-    }
-  }
-};
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32, 1) list_rows_kernel(const AttParams p) {
-  using L = RowLayout<D>;
+template <int D, bool LIST>
+__global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p) {
+  using L = RowLayout<D, LIST>;
   constexpr int E = L::ENTRIES, UPR = D / 8;
   extern __shared__ __align__(128) uint8_t smem_rows[];
   const int lane = lane_id();
   const int worker = warp_id() * gridDim.x + blockIdx.x;  // few workers: one per SM first
   const uint32_t ring = smem_u32(smem_rows) + warp_id() * L::WARP_BYTES;
+  Seg* segs = reinterpret_cast<Seg*>(smem_rows + L::OFF_SEG) + warp_id() * L::SEGS;
   volatile uint32_t* masks =
       reinterpret_cast<volatile uint32_t*>(smem_rows + L::OFF_MASK) + warp_id() * L::MASKS;
   asm volatile("griddepcontrol.launch_dependents;");  // the joining kernel may get ready
 
-  const int nt = (p.k + kGroup - 1) / kGroup;
-  Cursor cur;
+  Walk<LIST> walk;
   {
-    const int64_t total = static_cast<int64_t>(p.n_tok) * p.Hkv * nt;
-    const int64_t x0 = cut(p, p.workers, total, min(worker, p.workers));
-    const int64_t x1 = cut(p, p.workers, total, min(worker + 1, p.workers));
-    const int64_t unit = x0 / nt;
-    cur.t = static_cast<int>(unit / p.Hkv);
-    cur.j = static_cast<int>(unit % p.Hkv);
-    cur.i = static_cast<int>(x0 % nt);
-    cur.left = x1 - x0;
-    if (lane == 0 && worker < p.workers) {
-      int4 cont = make_int4(0, 0, 0, 0), open = make_int4(0, 0, 0, 0);
-      cont.x = cur.i > 0 && cur.left > 0;
-      const int64_t ue = x1 / nt;
-      if (x1 % nt != 0 && x1 > x0 && ue * nt >= x0) {
-        const int t = static_cast<int>(ue / p.Hkv);
-        const int b = __ldg(p.seq_of + t);
-        if (b >= 0 && b < p.n_seq)  // (else: left as it was)
-          open = make_int4(1, t, 1 | static_cast<int>(ue - static_cast<int64_t>(t) * p.Hkv) << 16,
-                           last_worker(p, p.workers, total, (ue + 1) * nt));
-      }
-      p.head[2 * worker] = cont;
-      p.head[2 * worker + 1] = open;
+    Start st;
+    if constexpr (LIST) {
+      st = list_start(p, worker, 1);
+    } else {
+      auto& ps = *reinterpret_cast<PlanShared<2 * kWarps>*>(smem_rows);  // before the first copies
+      plan_points<kWarps * 32>(p, ps, [&](int i) {
+        return (i >> 1) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) + (i & 1);
+      });
+      st = plan_start(ps, 2 * warp_id());
+      __syncthreads();
     }
+    if (lane == 0 && worker < p.workers) write_head<LIST>(p, st, worker);
+    walk.init(st, worker);
   }
 
   // ---- copies ahead.  A group passes three steps: token ids (a), table entries
-  // (b), copies (c); `ahead` is the next group whose ids are read.
+  // (b), copies (c).  The segments it meets go to the ring `segs` for the sums.
   const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
   struct Ahead {
-    int s, pg, pos, j, live;
+    int s, pg, j, live;
     const int32_t* bt;
   };
-  Cursor ahead = cur;
+  Seg as;  // the segment whose groups are being read
+  as.i1 = 0;
+  int ai = 0;          // its next group
+  const int32_t *abt = p.bts, *alist = p.idx;  // its block table, its list
+  uint32_t asegs = 0;  // segments met
+  bool ended = false;
   auto read_ids = [&](Ahead& a) {
     a.live = 0;
     a.s = -1;
-    a.pos = -1;
     a.j = 0;
     a.bt = p.bts;
-    if (ahead.left <= 0) return;
-    const int b = __ldg(p.seq_of + ahead.t);
-    if (b >= 0 && b < p.n_seq) {
-      const int e = ahead.i * kGroup + lane;
-      if (e < p.k) a.s = __ldg(p.idx + static_cast<int64_t>(ahead.t) * p.k + e);
-      a.pos = __ldg(p.positions + ahead.t);
-      a.bt = p.bts + static_cast<int64_t>(b) * p.max_blocks;
-    } else if (b >= p.n_seq) {
-      report(p.ctl, DEV_BAD_INPUT);
+    if (!ended && ai >= as.i1) {
+      walk.next(p, as);
+      ended = !as.valid;
+      if (lane == 0) segs[asegs % L::SEGS] = as;
+      ++asegs;
+      ai = as.i0;
+      if (!ended) {
+        abt = p.bts + static_cast<int64_t>(as.b) * p.max_blocks;
+        if (LIST) alist = p.idx + static_cast<int64_t>(as.m) * p.k + lane;
+      }
     }
-    a.j = ahead.j;
+    if (ended) return;
+    if constexpr (LIST) {
+      if (ai * kGroup + lane < p.k) a.s = __ldg(alist + ai * kGroup);
+      if (a.s > as.p0) a.s = -1;
+    } else {
+      a.s = as.key0(ai, 5) + lane;
+      if (a.s >= as.len) a.s = -1;  // rows past the sequence: zeros, whatever the cache holds
+    }
+    a.bt = abt;
+    a.j = as.j;
     a.live = 1;
-    ahead.step(p, nt);
+    ++ai;
   };
   auto read_page = [&](Ahead& a) {
-    a.pg = a.s >= 0 && a.s <= a.pos && a.s < cap ? __ldg(a.bt + (a.s >> p.page_shift)) : 0;
+    if (LIST && a.s >= cap) {
+      report(p.ctl, DEV_BAD_INPUT);
+      a.s = -1;
+    }
+    a.pg = a.s >= 0 ? __ldg(a.bt + (a.s >> p.page_shift)) : 0;
   };
   Ahead a0, a1, a2;  // copies next, table entry read, ids read
-  read_ids(a0);
-  read_page(a0);
-  read_ids(a1);
-  read_page(a1);
-  read_ids(a2);
+  a0.s = a1.s = a2.s = -1;
+  a0.live = a1.live = a2.live = 0;
+  a0.j = a1.j = a2.j = 0;
+  auto read_on = [&]() {
+    a0 = a1;
+    a1 = a2;
+    read_page(a1);
+    read_ids(a2);
+  };
+#pragma unroll 1
+  for (int i = 0; i < 3; ++i) read_on();
   int row = -1, head = 0, more = 0;  // cache row of this lane's token of the group being copied
-  uint32_t copied = 0;               // entries copied so far
-  // Copies the next entry (key rows, then value rows, of the next group).
-  auto copy_next = [&]() {
-    const bool keys = (copied & 1) == 0;
-    if (keys) {
-      row = -1;
-      more = a0.live;
-      head = a0.j;
-      if (a0.s >= 0 && a0.s <= a0.pos) {
-        int pg = a0.pg;
-        if (a0.s >= cap) {
-          report(p.ctl, DEV_BAD_INPUT);
-        } else {
-          if (pg < 0 || pg >= p.n_pages) {
-            report(p.ctl, DEV_BAD_INPUT);
-            pg = 0;
-          }
-          row = (pg << p.page_shift) | (a0.s & ((1 << p.page_shift) - 1));
-        }
+  uint32_t groups = 0, slot = 0;     // groups met by the copies; the ring's next entry
+  constexpr int PARTS = L::PARTS;
+  // The next group's cache rows, visible tokens and key head.
+  auto next_group = [&]() {
+    row = -1;
+    more = a0.live;
+    head = a0.j;
+    if (a0.s >= 0) {
+      int pg = a0.pg;
+      if (pg < 0 || pg >= p.n_pages) {
+        report(p.ctl, DEV_BAD_INPUT);
+        pg = 0;
       }
-      const uint32_t seen = __ballot_sync(0xffffffffu, row >= 0);
-      if (lane == 0) masks[(copied >> 1) % L::MASKS] = seen;
-      a0 = a1;
-      a1 = a2;
-      read_page(a1);
-      read_ids(a2);
+      row = (pg << p.page_shift) | (a0.s & ((1 << p.page_shift) - 1));
     }
+    const uint32_t seen = __ballot_sync(0xffffffffu, row >= 0);
+    if (lane == 0) masks[groups % L::MASKS] = seen;
+    ++groups;
+    read_on();
+  };
+  // Copies a part of the group's key or value rows into the next entry.
+  auto copy_rows = [&](const uint16_t* pool, int part) {
     if (more) {
-      const uint32_t dst = ring + (copied % E) * L::ENTRY;
-      const uint16_t* base = (keys ? p.kp : p.vp) + head * D + (lane % UPR) * 8;
+      const uint32_t dst = ring + slot * L::ENTRY;
+      const uint16_t* base = pool + head * D + (lane % UPR) * 8;
 #pragma unroll
-      for (int i = 0; i < UPR; ++i) {
+      for (int i = 0; i < UPR / PARTS; ++i) {
         const int r = i * (32 / UPR) + lane / UPR;
-        const int y = __shfl_sync(0xffffffffu, row, r);
+        const int y = __shfl_sync(0xffffffffu, row, part * L::TOKENS + r);
         cp_async16(dst + r * (D * 2) + (((lane % UPR) ^ (r & 7)) << 4),
                    base + static_cast<int64_t>(y < 0 ? 0 : y) * p.Hkv * D, y < 0 ? 0u : 16u);
       }
     }
     cp_async_commit();
-    ++copied;
+    slot = slot + 1 == E ? 0 : slot + 1;
   };
-#pragma unroll
-  for (int i = 0; i < E; ++i) copy_next();
+  // The entry that replaces part x of the keys (values) just summed: E entries on,
+  // which is 3 or 6 kinds on.
+  auto copy_keys = [&](int x) {
+    if (x == 0) next_group();
+    copy_rows(p.kp, x);
+  };
+  constexpr bool FLIP = (E / PARTS) & 1;
+#pragma unroll 1
+  for (int i = 0; i < E; ++i) {
+    const bool keys = (i / PARTS & 1) == 0;
+    if (keys && i % PARTS == 0) next_group();
+    copy_rows(keys ? p.kp : p.vp, i % PARTS);
+  }
 
   // ---- sums.  Lane: rows (heads) g and g + 8; columns 2 c, 2 c + 1 of each eight.
   const int g = lane >> 2, c = lane & 3;
-  uint32_t q[D / 16][4];
-  float o[D / 8][4];
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
   uint32_t done = 0;  // groups summed
-  int start = cur.i;  // first group of the segment
-  bool fresh = true, live = false;
-  while (cur.left > 0) {
-    if (fresh) {
-      const int b = __ldg(p.seq_of + cur.t);
-      live = b >= 0 && b < p.n_seq;
-      const uint16_t* qr = p.Q + (static_cast<int64_t>(cur.t) * p.H + cur.j * p.G) * D + 2 * c;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = g + 8 * (x & 1);
-          q[kk][x] = live && r < p.G
-                         ? __ldg(reinterpret_cast<const uint32_t*>(qr + r * D + kk * 16 + 8 * (x >> 1)))
-                         : 0u;
-        }
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) o[x][y] = 0.0f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.0f;
-      start = cur.i;
-      fresh = false;
-    }
-    const uint32_t ek = 2 * done;
-    cp_async_wait_group<E - 1>();
+  for (uint32_t sg = 0;; ++sg) {
     __syncwarp();
-    const uint32_t seen = masks[done % L::MASKS];
-    if (seen) {
-      // S: 16 heads x 32 tokens
-      float s[4][4];
-      const uint32_t kb = ring + (ek % E) * L::ENTRY;
+    const Seg& seg = segs[sg % L::SEGS];
+    if (!seg.valid) break;
+    const int rows = seg.toks * p.G, i1 = seg.i1;
+    uint32_t q[D / 16][4];
+    float o[D / 8][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int64_t orow[2];  // rows g and g + 8 of the results
+    int pos[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h, tok = r * p.g_inv >> 16;
+      orow[h] = static_cast<int64_t>(seg.tb + tok) * p.H + seg.j * p.G + r - tok * p.G;
+      pos[h] = seg.p0 + tok;
+    }
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
       for (int x = 0; x < 4; ++x)
+        q[kk][x] = g + 8 * (x & 1) < rows ? __ldg(reinterpret_cast<const uint32_t*>(
+                                                p.Q + orow[x & 1] * D + kk * 16 + 8 * (x >> 1) + 2 * c))
+                                          : 0u;
 #pragma unroll
-        for (int y = 0; y < 4; ++y) s[x][y] = 0.0f;
+    for (int x = 0; x < D / 8; ++x)
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
+      for (int y = 0; y < 4; ++y) o[x][y] = 0.0f;
+    for (int i = seg.i0; i < i1; ++i) {
+    const uint32_t seen = masks[done % L::MASKS];
+    // the next entry, once its rows are there (the ring holds E of them)
+    auto arrived = [&](uint32_t e) -> uint32_t {
+      cp_async_wait_group<E - 1>();
+      __syncwarp();
+      return ring + (e % E) * L::ENTRY;
+    };
+    // S: 16 heads x 32 tokens (nothing is summed where none is visible)
+    uint32_t at = 0;
+    float s[4][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {  // 16 tokens: matrices (tokens 0-7, 8-15) x (k 0-7, 8-15)
-          const int r = x * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, u = kk * 2 + (lane >> 4);
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) s[x][y] = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {  // 16 tokens: matrices (tokens 0-7, 8-15) x (k 0-7, 8-15)
+      if (x % (2 / PARTS) == 0) at = arrived(2 * PARTS * done + x / (2 / PARTS));
+      const uint32_t kb = at + (x % (2 / PARTS)) * 16 * D * 2;
+      if (seen) {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const int r = (lane & 7) + ((lane >> 3) & 1) * 8, u = kk * 2 + (lane >> 4);
           uint32_t b[4];
           ldsm4(kb + r * (D * 2) + ((u ^ (r & 7)) << 4), b);
           mma16816(s[2 * x], q[kk], b[0], b[2]);
           mma16816(s[2 * x + 1], q[kk], b[1], b[3]);
         }
-      __syncwarp();
-      copy_next();
-      if (seen != 0xffffffffu) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            if (!((seen >> (x * 8 + 2 * c + (y & 1))) & 1u)) s[x][y] = -INFINITY;
       }
-      uint32_t pa[2][4];
+      if (PARTS == 2 || x == 1) {
+        __syncwarp();
+        if constexpr (FLIP)
+          copy_rows(p.vp, PARTS == 2 ? x : 0);
+        else
+          copy_keys(PARTS == 2 ? x : 0);
+      }
+    }
+    uint32_t pa[2][4];
+    if (seen) {
+      if constexpr (LIST) {
+        if (seen != 0xffffffffu) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (!((seen >> (x * 8 + 2 * c + (y & 1))) & 1u)) s[x][y] = -INFINITY;
+        }
+      } else {
+        // groups that every row sees need no test
+        const int key0 = seg.key0(i, 5);
+        if (key0 + kGroup - 1 > seg.p0 ||
+            (p.window && key0 <= seg.p0 + seg.toks - 1 - p.window && key0 + kGroup > p.sinks)) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int key = key0 + x * 8 + 2 * c + (y & 1);
+              if (key > pos[y >> 1] || (p.window && key <= pos[y >> 1] - p.window && key >= p.sinks))
+                s[x][y] = -INFINITY;
+            }
+        }
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // rows g, g + 8
         float top = -INFINITY;
@@ -286,45 +328,43 @@ __global__ void __launch_bounds__(kWarps * 32, 1) list_rows_kernel(const AttPara
           pa[x >> 1][h + 2 * (x & 1)] = bf16x2(e0, e1);
         }
       }
-      cp_async_wait_group<E - 1>();
-      __syncwarp();
-      const uint32_t vb = ring + ((ek + 1) % E) * L::ENTRY;
+    }
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < 2; ++x) {
+      if (x % (2 / PARTS) == 0) at = arrived(2 * PARTS * done + PARTS + x / (2 / PARTS));
+      const uint32_t vb = at + (x % (2 / PARTS)) * 16 * D * 2;
+      if (seen) {
 #pragma unroll
         for (int d = 0; d < D / 16; ++d) {  // 16 columns: matrices (tokens 0-7, 8-15) x (8, 8)
-          const int r = x * 16 + (lane & 15), u = d * 2 + (lane >> 4);
+          const int r = lane & 15, u = d * 2 + (lane >> 4);
           uint32_t b[4];
           ldsm4_trans(vb + r * (D * 2) + ((u ^ (r & 7)) << 4), b);
           mma16816(o[2 * d], pa[x], b[0], b[1]);
           mma16816(o[2 * d + 1], pa[x], b[2], b[3]);
         }
-      __syncwarp();
-      copy_next();
-    } else {  // nothing visible among these tokens
-      copy_next();
-      cp_async_wait_group<E - 1>();
-      __syncwarp();
-      copy_next();
+      }
+      if (PARTS == 2 || x == 1) {
+        __syncwarp();
+        if constexpr (FLIP)
+          copy_keys(PARTS == 2 ? x : 0);
+        else
+          copy_rows(p.vp, PARTS == 2 ? x : 0);
+      }
     }
     ++done;
-    const int i = cur.i, t = cur.t, j = cur.j;
-    cur.step(p, nt);
-    if (i + 1 < nt && cur.left > 0) continue;
+    }
 
     // ---- the segment's result
-    fresh = true;
-    if (!live) continue;  // a row of no sequence: left as it was
-    const int part = start > 0 ? 2 * worker : i + 1 < nt ? 2 * worker + 1 : -1;
+    const int part = seg.part;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float sum = l[h];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const int r = g + 8 * h;
-      if (r >= p.G) continue;
+      if (r >= rows) continue;
       if (part >= 0) {
-        const int64_t at = static_cast<int64_t>(part) * kRows + r;
+        const int64_t at = static_cast<int64_t>(part) * kRowHeads + r;
         if (c == 0) *reinterpret_cast<float2*>(p.ml + 2 * at) = make_float2(m[h], sum);
 #pragma unroll
         for (int x = 0; x < D / 8; ++x)
@@ -332,35 +372,34 @@ __global__ void __launch_bounds__(kWarps * 32, 1) list_rows_kernel(const AttPara
               make_float2(o[x][2 * h], o[x][2 * h + 1]);
       } else {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int64_t at = static_cast<int64_t>(t) * p.H + j * p.G + r;
 #pragma unroll
         for (int x = 0; x < D / 8; ++x)
-          *reinterpret_cast<uint32_t*>(p.out + at * D + x * 8 + 2 * c) =
+          *reinterpret_cast<uint32_t*>(p.out + orow[h] * D + x * 8 + 2 * c) =
               bf16x2(o[x][2 * h] * inv, o[x][2 * h + 1] * inv);
-        if (p.lse && c == 0) p.lse[at] = row_lse(m[h], sum);
+        if (p.lse && c == 0) p.lse[orow[h]] = row_lse(m[h], sum);
       }
     }
   }
   cp_async_wait_all();
 }
 
-template <int D>
+template <int D, bool LIST>
 cudaError_t launch_rows(const AttParams& p, cudaStream_t s) {
-  using L = RowLayout<D>;
+  using L = RowLayout<D, LIST>;
+  auto kern = rows_kernel<D, LIST>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(ready.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(list_rows_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready.fetch_or(uint64_t{1} << dev);
   }
-  const int n = att_ctas();
-  list_rows_kernel<D><<<n, kWarps * 32, L::BYTES, s>>>(p);
+  kern<<<att_ctas(), kWarps * 32, L::BYTES, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.workers == 1) return e;
-  return launch_join<D>(p, kRows, 1, s);
+  return launch_join<D>(p, kRowHeads, 4, s);
 }
 
 }  // namespace
@@ -368,13 +407,16 @@ cudaError_t launch_rows(const AttParams& p, cudaStream_t s) {
 cudaError_t launch_attend_rows(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
   // at least 4 groups a worker: below that a unit falls into so many parts that
   // joining them costs more than the shorter stretches save (8 rows of 2048 tokens,
-  // 16 heads: 47 us with one group a worker, 18 us with four)
-  const int64_t groups =
-      static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kGroup - 1) / kGroup);
-  const int workers =
-      static_cast<int>(std::min<int64_t>(att_ctas() * kWarps, std::max<int64_t>(1, groups / 4)));
-  const AttParams p = att_params(a, ctl, workers);
-  return a.d == 128 ? launch_rows<128>(p, s) : launch_rows<64>(p, s);
+  // 16 heads: 47 us with one group a worker, 18 us with four).  The dense form finds
+  // its groups on the device.
+  int64_t workers = static_cast<int64_t>(att_ctas()) * kWarps;
+  if (a.idx) {
+    const int64_t groups = static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kGroup - 1) / kGroup);
+    workers = std::min(workers, std::max<int64_t>(1, groups / 4));
+  }
+  const AttParams p = att_params(a, ctl, static_cast<int>(workers), true);
+  if (a.idx) return a.d == 128 ? launch_rows<128, true>(p, s) : launch_rows<64, true>(p, s);
+  return a.d == 128 ? launch_rows<128, false>(p, s) : launch_rows<64, false>(p, s);
 }
 
 }  // namespace misa

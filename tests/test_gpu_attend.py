@@ -61,6 +61,11 @@ def _sample(n, most=24, seed=0):
     (12, 4, 128, 32, [257, 31], [600, 31]),                  # ragged row blocks
     (128, 1, 128, 64, [3], [515]),                           # the largest group
     (1, 1, 64, 16, [129], [400]),                            # a single head
+    (64, 2, 128, 64, [1] * 4, [900, 33, 2048, 1]),           # single tokens, groups of 32
+    (96, 2, 64, 16, [1, 2], [4000, 310]),                    # groups of 48
+    (16, 2, 128, 32, [2, 2, 1], [66, 32, 1000]),             # 16 rows a unit: two tokens of 8 heads
+    (4, 4, 64, 16, [16, 9, 0, 3], [16, 700, 5, 33]),         # one head a group, several tokens
+    (32, 2, 128, 128, [1, 1], [129, 6000]),                  # 16 heads a group
 ])
 def test_attend_matches_the_formula(lib, H, Hkv, d, page, q_lens, lens):
     cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, H, Hkv, d, page, seed=3)
@@ -74,6 +79,7 @@ def test_attend_matches_the_formula(lib, H, Hkv, d, page, q_lens, lens):
 @pytest.mark.parametrize("H,Hkv,d,page,q_lens,lens", [
     (8, 2, 128, 64, [1, 1, 1], [900, 50, 257]),
     (8, 2, 64, 16, [200, 3], [700, 3]),
+    (64, 1, 128, 32, [1, 1], [900, 300]),
 ])
 def test_attend_window_and_first_tokens(lib, window, sinks, H, Hkv, d, page, q_lens, lens):
     cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, H, Hkv, d, page, seed=5)
@@ -85,24 +91,26 @@ def test_attend_window_and_first_tokens(lib, window, sinks, H, Hkv, d, page, q_l
     check_rows(out, lse, _sample(len(seqs), 16), Q, cache, seqs, sees, H // Hkv, d ** -0.5)
 
 
-def test_attend_long_contexts_are_split_and_joined(lib):
+@pytest.mark.parametrize("H", [8, 64])
+def test_attend_long_contexts_are_split_and_joined(lib, H):
     # few rows over long caches: every unit is cut into parts by many CTAs
     q_lens, lens = [1, 2, 1], [40000, 9000, 12345]
-    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, 8, 2, 128, 64, seed=7)
+    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, H, 2, 128, 64, seed=7)
     out, lse = _run(lib, cache, Q, cu, ln)
-    check_rows(out, lse, range(4), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 4, 128 ** -0.5)
+    check_rows(out, lse, range(4), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), H // 2, 128 ** -0.5)
     again = _run(lib, cache, Q, cu, ln)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
-def test_attend_many_short_sequences(lib):
+@pytest.mark.parametrize("H", [4, 64])
+def test_attend_many_short_sequences(lib, H):
     rng = np.random.Generator(np.random.PCG64(11))
     n = 700                                    # more sequences than a CTA has threads
     q_lens = rng.integers(0, 4, n).tolist()
     lens = [q + int(x) for q, x in zip(q_lens, rng.integers(0, 90, n))]
-    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, 4, 2, 64, 16, seed=12)
+    cache, Q, cu, ln, seqs, pos = _batch(q_lens, lens, H, 2, 64, 16, seed=12)
     out, lse = _run(lib, cache, Q, cu, ln)
-    check_rows(out, lse, _sample(len(seqs), 120), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 2,
+    check_rows(out, lse, _sample(len(seqs), 120), Q, cache, seqs, lambda t: slice(0, pos[t] + 1), H // 2,
                64 ** -0.5)
 
 
