@@ -382,6 +382,7 @@ int misa_release_pages(const int32_t* release, int32_t* seq_lens, const int32_t*
  * [n, H] = max |row| / 448 (1 where that is 0), codes = e4m3(row / scale): the
  * operands of misa_score_tokens_fp8.  A row that is not finite is reported as
  * MISA_ERR_DEVICE.  Rows with a negative position are left as they were.
+ * Results overlap no input, but for Y == X.
  */
 int misa_rope(const uint16_t* X, const int32_t* positions, const double* inv_freq, int n, int H,
               int d, int rope_dim, int offset, int interleaved, float amplitude, int transpose,
@@ -433,7 +434,8 @@ int misa_rope_frequencies(int rope_dim, double base, int scaling, double factor,
  *   Q, out [n_tok, H, d] bf16; k_pages, v_pages [n_pages, page_size, H_kv, d] bf16;
  *   block_tables [n_seq, max_blocks], cu_q [n_seq + 1], seq_lens [n_seq] int32
  *   (device); d in {64, 128}, H_kv divides H, G <= 128, page_size 16, 32, 64 or
- *   128 (else MISA_ERR_UNSUPPORTED); scale > 0; sinks need a window.
+ *   128 (else MISA_ERR_UNSUPPORTED); scale > 0; sinks need a window.  Entries of
+ *   cu_q ascend; those past n_tok are taken as n_tok.
  * One call serves prefill chunks, single new tokens and mixed batches; rows past
  * cu_q[n_seq] are left as they were.  A row that sees nothing gives zeros and an
  * lse of -inf.  Products take bf16 operands with fp32 sums; the weights are

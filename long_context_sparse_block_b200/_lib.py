@@ -667,6 +667,8 @@ def misa_rope(x, positions, inv_freq, offset: int = 0, interleaved: bool = False
     dev, d = x.get_device(), x.shape[2]
     if out is None:
         out = torch.empty_like(x)
+    if x.shape[0] == 0:
+        return out
     a = _rope_args(x, positions, inv_freq, offset, interleaved, amplitude, dev, d)
     st = _lib.misa_rope(*a, int(bool(transpose)), _arg(out, x.numel(), _BF16_CODES, "out", dev),
                         _raw_stream(dev))
@@ -685,6 +687,8 @@ def misa_rope_fp8(x, positions, inv_freq, offset: int = 0, interleaved: bool = F
         codes = torch.empty((n, H, d), dtype=torch.uint8, device=x.device)
     if scale is None:
         scale = torch.empty((n, H), dtype=torch.float32, device=x.device)
+    if n == 0:
+        return codes, scale
     a = _rope_args(x, positions, inv_freq, offset, interleaved, amplitude, dev, d)
     st = _lib.misa_rope_fp8(*a, _arg(codes, n * H * d, _E4M3_CODES, "codes", dev),
                             _arg(scale, n * H, _F32, "scale", dev), _raw_stream(dev))
@@ -712,6 +716,8 @@ def misa_cache_append(k, positions, slots, inv_freq, k_pages, k_scale=None, v=No
         pvp = _arg(v_pages, rows * d, _BF16_CODES, "v_pages", dev)
     if kd == MISA_K_FP8E4M3 and k_scale is None:
         raise ValueError("e4m3 pages need k_scale")
+    if k.shape[0] == 0:
+        return
     a = _rope_args(k, positions, inv_freq, offset, interleaved, amplitude, dev, d)
     st = _lib.misa_cache_append(
         a[0], pv, a[1], _arg(slots, k.shape[0], _I32, "slots", dev), *a[2:], kd,
@@ -740,6 +746,8 @@ def _attend_args(Q, k_pages, v_pages, block_tables, scale, out, want_lse, lse, w
         out = torch.empty_like(Q)
     if lse is None and want_lse:
         lse = Q.new_empty((n_tok, H), dtype=torch.float32)
+    if n_tok == 0 or n_seq == 0:
+        return None, None, None, None, out, lse, dev
     pages = (_arg(Q, 0, _BF16_CODES, "Q", dev), _arg(k_pages, 0, _BF16_CODES, "k_pages", dev),
              _arg(v_pages, 0, _BF16_CODES, "v_pages", dev),
              _arg(block_tables, 0, _I32, "block_tables", dev), max_blocks, page_size, n_pages)
@@ -771,6 +779,8 @@ def misa_attend_paged(Q, k_pages, v_pages, block_tables, cu_q, seq_lens, scale: 
     they were.  ws: misa_workspace_size("attend", 1, 0, d, 0) bytes, allocated when None."""
     pages, sizes, results, work, out, lse, dev = _attend_args(Q, k_pages, v_pages, block_tables,
                                                               scale, out, want_lse, lse, ws)
+    if pages is None:   # no rows
+        return out, lse
     n_seq, n_tok, H, Hkv, d, scale = sizes
     st = _lib.misa_attend_paged(*pages, _arg(cu_q, n_seq + 1, _I32, "cu_q", dev),
                                 _arg(seq_lens, n_seq, _I32, "seq_lens", dev), n_seq, n_tok, H, Hkv, d,
@@ -789,6 +799,8 @@ def misa_attend_selected(Q, k_pages, v_pages, block_tables, seq_of, positions, i
         raise ValueError("idx must be [n_tok, k]")
     pages, sizes, results, work, out, lse, dev = _attend_args(Q, k_pages, v_pages, block_tables,
                                                               scale, out, want_lse, lse, ws)
+    if pages is None:   # no rows
+        return out, lse
     n_seq, n_tok, H, Hkv, d, scale = sizes
     k = idx.shape[1]
     st = _lib.misa_attend_selected(*pages, _arg(seq_of, n_tok, _I32, "seq_of", dev),

@@ -742,10 +742,11 @@ int misa_plan_step(const int32_t* q_lens, const int32_t* ctx_lens, int n_seq, in
                    int32_t* cu_q, int32_t* seq_lens, int32_t* positions, int32_t* slots,
                    int32_t* seq_of, int32_t* granted, int32_t* free_count_out, void* stream) {
   if (n_seq < 0 || n_tok < 0 || max_blocks < 1) return MISA_ERR_INVALID_ARG;
+  if (!cu_q || !aligned4(cu_q)) return MISA_ERR_INVALID_ARG;
   for (const void* q : {static_cast<const void*>(q_lens), static_cast<const void*>(ctx_lens),
-                        static_cast<const void*>(block_tables), static_cast<const void*>(cu_q),
-                        static_cast<const void*>(seq_lens), static_cast<const void*>(granted)})
-    if (!q || !aligned4(q)) return MISA_ERR_INVALID_ARG;
+                        static_cast<const void*>(block_tables), static_cast<const void*>(seq_lens),
+                        static_cast<const void*>(granted)})
+    if (n_seq > 0 && (!q || !aligned4(q))) return MISA_ERR_INVALID_ARG;
   for (const void* q : {static_cast<const void*>(positions), static_cast<const void*>(slots),
                         static_cast<const void*>(seq_of)})
     if (n_tok > 0 && (!q || !aligned4(q))) return MISA_ERR_INVALID_ARG;

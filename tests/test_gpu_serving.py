@@ -176,3 +176,41 @@ def test_a_captured_decode_step(lib):
         lens = [42 + i, 72 + i, 102 + i]
         assert ses.lens.tolist() == lens and p.positions.tolist() == [x - 1 for x in lens]
         _check_out(ses, out, lse, q, idx, [0, 1, 2], [x - 1 for x in lens])
+
+
+def test_first_use_inside_a_capture(lib):
+    # a process whose first calls are captured: nothing may need a warm-up outside
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+from long_context_sparse_block_b200 import _lib as lib
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+bf = lambda *s: torch.randn(s, device="cuda").to(torch.bfloat16)
+q, one = bf(2, 4, 64), i32(1, 1)
+kp, vp, tables = bf(8, 16, 2, 64), bf(8, 16, 2, 64), torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+lens, idx = i32(20, 7), torch.tensor([[0, 3, 20], [7, 2, -1]], dtype=torch.int32, device="cuda")
+f, _ = lib.misa_rope_frequencies(32)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    p = lib.misa_plan_step(one, lens, tables, 16, n_tok=2)
+    r = lib.misa_rope(q, p.positions, f)
+    lib.misa_cache_append(r[:, :2].contiguous(), p.positions, p.slots, f, kp)
+    a, _ = lib.misa_attend_paged(r, kp, vp, tables, p.cu_q, p.seq_lens)
+    b, _ = lib.misa_attend_selected(r, kp, vp, tables, p.seq_of, p.positions, idx)
+    big = r.repeat(1, 16, 1)
+    c, _ = lib.misa_attend_paged(big, kp, vp, tables, p.cu_q, p.seq_lens)
+    d, _ = lib.misa_attend_selected(big, kp, vp, tables, p.seq_of, p.positions, idx)
+g.replay()
+torch.cuda.synchronize()
+assert lib.misa_last_device_status() == 0
+for x in (a, b, c, d):
+    assert torch.isfinite(x.float()).all()
+assert p.positions.tolist() == [20, 7]
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), r.stderr[-2000:]

@@ -176,3 +176,33 @@ def test_binding_checks_sizes_before_devices(lib):
         lib.misa_cache_append(bf(4, 3, 64), i32(4), i32(4), f, pages)
     with pytest.raises(ValueError):
         lib.misa_plan_step(i32(4), i32(4), i32(4, 8), 16)
+
+
+def test_calls_without_rows_do_nothing(lib):
+    import torch
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    f = torch.zeros(32, dtype=torch.float64)
+    pages = bf(10, 16, 2, 64)
+    assert lib.misa_rope(bf(0, 2, 64), i32(0), f).shape == (0, 2, 64)
+    codes, scale = lib.misa_rope_fp8(bf(0, 2, 64), i32(0), f)
+    assert codes.shape == (0, 2, 64) and scale.shape == (0, 2)
+    assert lib.misa_cache_append(bf(0, 2, 64), i32(0), i32(0), f, pages) is None
+    out, lse = lib.misa_attend_paged(bf(0, 4, 64), pages, pages, i32(2, 8), i32(3), i32(2), want_lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    out, lse = lib.misa_attend_selected(bf(0, 4, 64), pages, pages, i32(2, 8), i32(0), i32(0), i32(0, 9))
+    assert out.shape == (0, 4, 64) and lse is None
+
+
+def test_tensors_of_another_device_are_refused(lib, monkeypatch):
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="the current device is cuda:1"):
+        lib._raw_stream(0)
+
+    class There:                        # a tensor as the checks see it, on cuda:1
+        dtype = torch.int32
+        numel = staticmethod(lambda: 8)
+        get_device = staticmethod(lambda: 1)
+    with pytest.raises(ValueError, match="is on cuda:1"):
+        lib._arg(There, 4, (torch.int32,), "x", 0)
