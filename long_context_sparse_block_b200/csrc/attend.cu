@@ -16,26 +16,35 @@
 // the tensor cores ask for (relative 2^-8 per weight, averaged over the sum).
 //
 // Rows.  The G = H / Hkv query heads that share a key head are rows of one
-// matrix: row r of (sequence, key head) is query r / G, head r % G, so every key
-// tile serves 128 rows even for few tokens.  A unit is (sequence, block of 256
-// rows, key head); its two slots are two 128-row halves, each with its own
-// softmax warpgroup, S / P and O: while one slot's rows are exponentiated the
-// tensor cores work for the other.  A unit of at most 128 rows (decode, ragged
-// ends, the list form) uses the two slots for the same rows and alternate tiles
-// instead, which keeps the same overlap, and joins the two O in TMEM at the end.
+// matrix: a slot of 128 rows holds T = 128 / G tokens, head by head, so every key
+// tile serves up to 128 rows even for few tokens.  A unit is (sequence, 2 T tokens,
+// key head); its two slots have a softmax warpgroup, S / P and O each: while one
+// slot's rows are exponentiated the tensor cores work for the other.  A unit of at
+// most T tokens (ragged ends, the list form) uses the two slots for the same rows
+// and alternate tiles instead, which keeps the overlap, and joins the two O in TMEM.
 //
-// Split.  The units' cost (a closed form, linear in the row block) is laid on a
-// line that is cut evenly over the CTAs; a unit cut by a boundary leaves
-// unnormalised O, m and l of each part in the workspace (at most two parts per
-// CTA) and a second kernel joins them in a fixed order.  So one new token over a
-// long cache fills the chip as well as a long chunk does, lengths stay on the
-// device, and results do not depend on timing.
+// Split.  The units' cost (a closed form, linear in the block) is laid on a line
+// that is cut evenly over the CTAs; a unit cut by a boundary leaves unnormalised O,
+// m and l of each part in the workspace (at most two parts per CTA) and a second
+// kernel joins them in a fixed order.  So a few new tokens over a long cache fill
+// the chip as well as a long chunk does, lengths stay on the device, and results do
+// not depend on timing.
 //
-// Warps: 0 key / value loader (TMA boxes, one per page, through the block
-// table; the list form loads rows by cp.async from four warps of its own),
-// 1 MMA issuer, 3 scheduler, 2 query loader (and the zeroing of value rows past the end of
-// a sequence, which may hold anything, before the MMA reads them: 0 * NaN is
-// NaN), 4-7 and 8-11 the softmax of slots 0 and 1.
+// Warps: 0 key / value loader (TMA boxes, one per page, through the block table;
+// the list form loads rows by cp.async from four warps of its own), 1 MMA issuer,
+// 2 query loader (and the zeroing of value rows past the end of a sequence, which
+// may hold anything, before the MMA reads them: 0 * NaN is NaN), 3 scheduler, 4-7
+// and 8-11 the softmax of slots 0 and 1.
+//
+// Measured: 2048 new tokens at the end of 32768 keys, 32 heads of 128 on 4 key
+// heads: 834 us = 1278 TFLOP/s, 76 % of the measured bf16 rate; sustained for a
+// second, under the power cap, 957 us (80 % of the sustained rate).  A step (one
+// tile for both slots) takes 1.95 us: 2048 cycles of products and as many of the
+// special-function unit, half busy each, behind the chain S, maximum, exponentials,
+// P V of a slot.  Exponentials on the FMA pipe instead (degree 5, 3, 5 or 8 of 16)
+// measured 880, 899 and 967 against 853 us: issue slots, not that unit, are short.
+// The list form gathers 4096 lists of 2048 tokens (64 heads on one key head) in 570
+// us: 7.5 TB/s of rows out of L2.
 #include <atomic>
 #include <cstring>
 
@@ -69,10 +78,11 @@ struct AttLayout {
   static_assert(ALLOC <= 232448, "shared memory of an SM");
 };
 
-// List form: with 8 units or more for a CTA, units are left whole (the CTAs' work
-// then differs by one unit at most) and nothing has to be joined.
+// List form: with 8 units or more for a CTA, or units of one or two tiles, units are
+// left whole (the CTAs' work then differs by one unit at most) and nothing has to be
+// joined.
 __host__ __device__ inline bool whole_units(const AttParams& p, int ctas) {
-  return static_cast<int64_t>(p.n_tok) * p.Hkv >= 8ll * ctas;
+  return p.k <= 2 * kTile || static_cast<int64_t>(p.n_tok) * p.Hkv >= static_cast<int64_t>(8) * ctas;
 }
 
 // The low n bits (n clamped to 0..32).
@@ -225,268 +235,268 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
 
   if (warp < 4) {
     if constexpr (LIST) reg_dec<64>(); else reg_dec<72>();
-  if (warp == 0) {
-    if constexpr (!LIST) {
-      // -------------------------------------------------------- key / value loader
+    if (warp == 0) {
+      if constexpr (!LIST) {
+        // -------------------------------------------------------- key / value loader
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const int page = 1 << p.page_shift, per = kTile / page;
+        for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
+          const Seg g = seg_at(sg);
+          __syncwarp();
+          if (lane == 0) seg_done(sg);
+          const int n = g.i1 - g.i0;
+          const int32_t* bt = p.bts + static_cast<int64_t>(g.b) * p.max_blocks;
+          auto page_row = [&](int x) -> int {  // this lane's page of tile x
+            if (lane >= per || x >= n) return 0;
+            const int64_t s0 = static_cast<int64_t>(g.key0(g.i0 + x, 7)) + lane * page;
+            int64_t y = p.key_rows;  // past the sequence: a box of fill rows
+            if (s0 < g.len) {
+              int64_t pg = __ldg(bt + (s0 >> p.page_shift));
+              if (pg < 0 || pg >= p.n_pages) {
+                report(p.ctl, DEV_BAD_INPUT);
+                pg = 0;
+              }
+              y = pg << p.page_shift;
+            }
+            return static_cast<int>(y);
+          };
+          auto load = [&](const CUtensorMap* map, int y) -> bool {
+            if (!warp_wait(bar(EMPTY + stage), phase ^ 1, abort_flag, p.ctl)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(bar(FULL + stage), L::TILE);
+            __syncwarp();
+            if (lane < per) {
+#pragma unroll
+              for (int c = 0; c < L::CH; ++c)
+                tma_load_3d(sKV + stage * L::TILE + c * L::CHUNK + lane * page * 128, map,
+                            bar(FULL + stage), c * 64, g.j, y);
+            }
+            if (++stage == ST) {
+              stage = 0;
+              phase ^= 1;
+            }
+            return true;
+          };
+          int y_cur = page_row(0), y_next = page_row(1), y_prev = 0;
+          // the order in which the MMA warp takes them (see there)
+          for (int x = 0; x < n + g.split && ok; ++x) {
+            if (x < n) ok = load(&kmap, y_cur);
+            if (!g.split)
+              ok = ok && load(&vmap, y_cur);
+            else if (ok && x > 0)
+              ok = load(&vmap, y_prev);
+            y_prev = y_cur;
+            y_cur = y_next;
+            y_next = page_row(x + 2);
+          }
+          if (!ok) break;
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp runs the control flow, so that descriptors and addresses
+      // stay warp-uniform; one elected lane issues.  (With everything under
+      // `lane == 0` the issue of a step took 4200 cycles instead of 2048 of
+      // tensor work.)
+      const bool leader = elect_one();
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t phase = 0, tails = 0;
+      uint32_t used[2] = {0, 0};   // segments in which the slot had tiles
+      uint32_t pcount[2] = {0, 0}; // tiles of the slot so far
       bool ok = true;
-      const int page = 1 << p.page_shift, per = kTile / page;
+      constexpr uint32_t id_qk = umma_idesc_bf16_f32(kTile, kTile);
+      constexpr uint32_t id_pv = umma_idesc_bf16_f32(kTile, D) | (1u << 16);  // B is MN-major
+      const uint64_t dq = umma_desc_kmajor(sQ, 128), dk = umma_desc_kmajor(sKV, 128),
+                     dv = umma_desc_mnmajor(sKV, L::CHUNK);
+      auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.ctl); };
+      auto commit = [&](int i) {
+        if (leader) tc_commit(bar(i));
+      };
+      for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
+        const Seg& gs = seg_at(sg);
+        const int n = __shfl_sync(0xffffffffu, gs.i1 - gs.i0, 0);
+        const bool split = __shfl_sync(0xffffffffu, gs.split, 0) != 0;
+        const int key0 = gs.key0(gs.i1 - 1, 7);
+        const bool tail =
+            __shfl_sync(0xffffffffu, !LIST && gs.len > key0 && gs.len < key0 + kTile, 0) != 0;
+        __syncwarp();
+        if (lane == 0) seg_done(sg);
+        bool told = !tail;
+        int at = 0;  // ring entries of this segment waited for
+        // The next ring entry's stage, once its tile is there.
+        auto next = [&](int& st) -> bool {
+          if (!wait(FULL + stage, phase)) return false;
+          st = stage;
+          if (++stage == ST) {
+            stage = 0;
+            phase ^= 1;
+          }
+          ++at;
+          // the entry that the last tile's values replace has been seen: their
+          // phase can be waited for by parity
+          if (!told && at + ST >= 2 * n) {
+            if (lane == 0) mbar_arrive(bar(VTAIL));
+            told = true;
+          }
+          if (LIST) fence_proxy_async_smem();
+          tc_fence_after();
+          return true;
+        };
+        auto qk = [&](int slot, int st) {  // S of the slot
+          const uint64_t a = dq + (split ? 0 : slot) * (L::QTILE >> 4);
+          const uint64_t b = dk + st * (L::TILE >> 4);
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = ((kk / 4) * L::CHUNK + (kk % 4) * 32) >> 4;
+              tc_mma_bf16(tmem_base + slot * kTile, a + o, b + o, id_qk, kk > 0 ? 1u : 0u);
+            }
+          }
+        };
+        auto pv = [&](int slot, int st, bool first) -> bool {  // O += P V of the slot
+          const uint64_t b = dv + st * (L::TILE >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {  // the first half of P is there early
+            if (!wait(PFULL + 2 * slot + half, pcount[slot] & 1)) return false;
+            tc_fence_after();
+            if (leader) {
+#pragma unroll
+              for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+                tc_mma_bf16_ta(tmem_base + 256 + slot * D, tmem_base + slot * kTile + kk * 8,
+                               b + kk * (2048 >> 4), id_pv, kk > 0 || !first ? 1u : 0u);
+            }
+          }
+          ++pcount[slot];
+          return true;
+        };
+        auto tail_ready = [&]() -> bool {  // rows past the sequence have been zeroed
+          if (!wait(VREADY, tails & 1)) return false;
+          fence_proxy_async_smem();
+          ++tails;
+          return true;
+        };
+        ok = wait(QFULL, sg & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (split) {
+          for (int x = -2; x < n && ok; ++x) {
+            const int slot = x & 1;
+            int st;
+            if (x >= 0) {
+              ok = next(st) && (x < n - 1 || !tail || tail_ready()) &&
+                   (x > 1 || wait(OEMPTY + slot, (used[slot] & 1) ^ 1)) && pv(slot, st, x < 2);
+              if (!ok) break;
+              commit(EMPTY + st);
+              if (x + 2 >= n) commit(OFULL + slot);
+            }
+            if (x + 2 < n) {
+              ok = next(st);
+              if (!ok) break;
+              qk(slot, st);
+              commit(EMPTY + st);
+              commit(SFULL + slot);
+              if (x + 3 == n) commit(QEMPTY);  // the query rows are free again
+            }
+          }
+          ++used[0];
+          if (n > 1) ++used[1];
+        } else {
+          int sk = 0, sv;
+          for (int i = -1; i < n && ok; ++i) {
+            if (i >= 0) {
+              ok = next(sv) && (i < n - 1 || !tail || tail_ready()) &&
+                   (i > 0 || wait(OEMPTY, (used[0] & 1) ^ 1)) && pv(0, sv, i == 0);
+              if (!ok) break;
+              if (i == n - 1) commit(OFULL);
+            }
+            if (i + 1 < n) {
+              ok = next(sk);
+              if (!ok) break;
+              qk(0, sk);
+              commit(SFULL);
+            }
+            if (i >= 0) {
+              ok = (i > 0 || wait(OEMPTY + 1, (used[1] & 1) ^ 1)) && pv(1, sv, i == 0);
+              if (!ok) break;
+              commit(EMPTY + sv);
+              if (i == n - 1) commit(OFULL + 1);
+            }
+            if (i + 1 < n) {
+              qk(1, sk);
+              commit(EMPTY + sk);
+              commit(SFULL + 1);
+              if (i + 2 == n) commit(QEMPTY);
+            }
+          }
+          ++used[0];
+          ++used[1];
+        }
+        if (!ok) break;
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ scheduler
+      if (lane == 0) {
+        Walk<LIST> walk;
+        walk.init(st, blockIdx.x);
+        for (;; ++sg) {
+          if (!mbar_wait(bar(GEMPTY + sg % kSegs), ((sg / kSegs) & 1) ^ 1, abort_flag, p.ctl)) break;
+          Seg g;
+          walk.next(p, g);
+          segs[sg % kSegs] = g;
+          mbar_arrive(bar(GFULL + sg % kSegs));
+          if (sg == 0) write_head<LIST>(p, st, blockIdx.x);
+          if (!g.valid) break;
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ------------------------------------------------------------ query loader, value tails
+      uint32_t ring = 0, tails = 0;
+      bool ok = true;
       for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
         const Seg g = seg_at(sg);
         __syncwarp();
         if (lane == 0) seg_done(sg);
         const int n = g.i1 - g.i0;
-        const int32_t* bt = p.bts + static_cast<int64_t>(g.b) * p.max_blocks;
-        auto page_row = [&](int x) -> int {  // this lane's page of tile x
-          if (lane >= per || x >= n) return 0;
-          const int64_t s0 = static_cast<int64_t>(g.key0(g.i0 + x, 7)) + lane * page;
-          int64_t y = p.key_rows;  // past the sequence: a box of fill rows
-          if (s0 < g.len) {
-            int64_t pg = __ldg(bt + (s0 >> p.page_shift));
-            if (pg < 0 || pg >= p.n_pages) {
-              report(p.ctl, DEV_BAD_INPUT);
-              pg = 0;
-            }
-            y = pg << p.page_shift;
-          }
-          return static_cast<int>(y);
-        };
-        auto load = [&](const CUtensorMap* map, int y) -> bool {
-          if (!warp_wait(bar(EMPTY + stage), phase ^ 1, abort_flag, p.ctl)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(bar(FULL + stage), L::TILE);
-          __syncwarp();
-          if (lane < per) {
+        if (!warp_wait(bar(QEMPTY), (sg & 1) ^ 1, abort_flag, p.ctl)) break;
+        // a slot's T tokens x G heads as one box per 64 elements; tokens past the
+        // unit's belong to others and stay in their own rows of S
+        if (lane == 0) {
+          if (sg == 0) fence_proxy_async_smem();  // the plan's words lay where the rows go
+          const int slots = g.split ? 1 : 2, toks = LIST ? 1 : p.T;
+          mbar_arrive_expect_tx(bar(QFULL), slots * L::CH * toks * p.G * 128);
+          for (int i = 0; i < slots; ++i)
 #pragma unroll
             for (int c = 0; c < L::CH; ++c)
-              tma_load_3d(sKV + stage * L::TILE + c * L::CHUNK + lane * page * 128, map,
-                          bar(FULL + stage), c * 64, g.j, y);
-          }
-          if (++stage == ST) {
-            stage = 0;
-            phase ^= 1;
-          }
-          return true;
-        };
-        int y_cur = page_row(0), y_next = page_row(1), y_prev = 0;
-        // the order in which the MMA warp takes them (see there)
-        for (int x = 0; x < n + g.split && ok; ++x) {
-          if (x < n) ok = load(&kmap, y_cur);
-          if (!g.split)
-            ok = ok && load(&vmap, y_cur);
-          else if (ok && x > 0)
-            ok = load(&vmap, y_prev);
-          y_prev = y_cur;
-          y_cur = y_next;
-          y_next = page_row(x + 2);
+              tma_load_3d(sQ + i * L::QTILE + c * L::CHUNK, &qmap, bar(QFULL), c * 64, g.j * p.G,
+                          g.tb + i * p.T);
         }
-        if (!ok) break;
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the control flow, so that descriptors and addresses
-    // stay warp-uniform; one elected lane issues.  (With everything under
-    // `lane == 0` the issue of a step took 4200 cycles instead of 2048 of
-    // tensor work.)
-    const bool leader = elect_one();
-    int stage = 0;
-    uint32_t phase = 0, tails = 0;
-    uint32_t used[2] = {0, 0};   // segments in which the slot had tiles
-    uint32_t pcount[2] = {0, 0}; // tiles of the slot so far
-    bool ok = true;
-    constexpr uint32_t id_qk = umma_idesc_bf16_f32(kTile, kTile);
-    constexpr uint32_t id_pv = umma_idesc_bf16_f32(kTile, D) | (1u << 16);  // B is MN-major
-    const uint64_t dq = umma_desc_kmajor(sQ, 128), dk = umma_desc_kmajor(sKV, 128),
-                   dv = umma_desc_mnmajor(sKV, L::CHUNK);
-    auto wait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, abort_flag, p.ctl); };
-    auto commit = [&](int i) {
-      if (leader) tc_commit(bar(i));
-    };
-    for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
-      const Seg& gs = seg_at(sg);
-      const int n = __shfl_sync(0xffffffffu, gs.i1 - gs.i0, 0);
-      const bool split = __shfl_sync(0xffffffffu, gs.split, 0) != 0;
-      const int key0 = gs.key0(gs.i1 - 1, 7);
-      const bool tail =
-          __shfl_sync(0xffffffffu, !LIST && gs.len > key0 && gs.len < key0 + kTile, 0) != 0;
-      __syncwarp();
-      if (lane == 0) seg_done(sg);
-      bool told = !tail;
-      int at = 0;  // ring entries of this segment waited for
-      // The next ring entry's stage, once its tile is there.
-      auto next = [&](int& st) -> bool {
-        if (!wait(FULL + stage, phase)) return false;
-        st = stage;
-        if (++stage == ST) {
-          stage = 0;
-          phase ^= 1;
-        }
-        ++at;
-        // the entry that the last tile's values replace has been seen: their
-        // phase can be waited for by parity
-        if (!told && at + ST >= 2 * n) {
-          if (lane == 0) mbar_arrive(bar(VTAIL));
-          told = true;
-        }
-        if (LIST) fence_proxy_async_smem();
-        tc_fence_after();
-        return true;
-      };
-      auto qk = [&](int slot, int st) {  // S of the slot
-        const uint64_t a = dq + (split ? 0 : slot) * (L::QTILE >> 4);
-        const uint64_t b = dk + st * (L::TILE >> 4);
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t o = ((kk / 4) * L::CHUNK + (kk % 4) * 32) >> 4;
-            tc_mma_bf16(tmem_base + slot * kTile, a + o, b + o, id_qk, kk > 0 ? 1u : 0u);
-          }
-        }
-      };
-      auto pv = [&](int slot, int st, bool first) -> bool {  // O += P V of the slot
-        const uint64_t b = dv + st * (L::TILE >> 4);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {  // the first half of P is there early
-          if (!wait(PFULL + 2 * slot + half, pcount[slot] & 1)) return false;
-          tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-              tc_mma_bf16_ta(tmem_base + 256 + slot * D, tmem_base + slot * kTile + kk * 8,
-                             b + kk * (2048 >> 4), id_pv, kk > 0 || !first ? 1u : 0u);
-          }
-        }
-        ++pcount[slot];
-        return true;
-      };
-      auto tail_ready = [&]() -> bool {  // rows past the sequence have been zeroed
-        if (!wait(VREADY, tails & 1)) return false;
-        fence_proxy_async_smem();
-        ++tails;
-        return true;
-      };
-      ok = wait(QFULL, sg & 1);
-      if (!ok) break;
-      tc_fence_after();
-      if (split) {
-        for (int x = -2; x < n && ok; ++x) {
-          const int slot = x & 1;
-          int st;
-          if (x >= 0) {
-            ok = next(st) && (x < n - 1 || !tail || tail_ready()) &&
-                 (x > 1 || wait(OEMPTY + slot, (used[slot] & 1) ^ 1)) && pv(slot, st, x < 2);
-            if (!ok) break;
-            commit(EMPTY + st);
-            if (x + 2 >= n) commit(OFULL + slot);
-          }
-          if (x + 2 < n) {
-            ok = next(st);
-            if (!ok) break;
-            qk(slot, st);
-            commit(EMPTY + st);
-            commit(SFULL + slot);
-            if (x + 3 == n) commit(QEMPTY);  // the query rows are free again
-          }
-        }
-        ++used[0];
-        if (n > 1) ++used[1];
-      } else {
-        int sk = 0, sv;
-        for (int i = -1; i < n && ok; ++i) {
-          if (i >= 0) {
-            ok = next(sv) && (i < n - 1 || !tail || tail_ready()) &&
-                 (i > 0 || wait(OEMPTY, (used[0] & 1) ^ 1)) && pv(0, sv, i == 0);
-            if (!ok) break;
-            if (i == n - 1) commit(OFULL);
-          }
-          if (i + 1 < n) {
-            ok = next(sk);
-            if (!ok) break;
-            qk(0, sk);
-            commit(SFULL);
-          }
-          if (i >= 0) {
-            ok = (i > 0 || wait(OEMPTY + 1, (used[1] & 1) ^ 1)) && pv(1, sv, i == 0);
-            if (!ok) break;
-            commit(EMPTY + sv);
-            if (i == n - 1) commit(OFULL + 1);
-          }
-          if (i + 1 < n) {
-            qk(1, sk);
-            commit(EMPTY + sk);
-            commit(SFULL + 1);
-            if (i + 2 == n) commit(QEMPTY);
-          }
-        }
-        ++used[0];
-        ++used[1];
-      }
-      if (!ok) break;
-    }
-    __syncwarp();
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ scheduler
-    if (lane == 0) {
-      Walk<LIST> walk;
-      walk.init(st, blockIdx.x);
-      for (;; ++sg) {
-        if (!mbar_wait(bar(GEMPTY + sg % kSegs), ((sg / kSegs) & 1) ^ 1, abort_flag, p.ctl)) break;
-        Seg g;
-        walk.next(p, g);
-        segs[sg % kSegs] = g;
-        mbar_arrive(bar(GFULL + sg % kSegs));
-        if (sg == 0) write_head<LIST>(p, st, blockIdx.x);
-        if (!g.valid) break;
-      }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ query loader, value tails
-    uint32_t ring = 0, tails = 0;
-    bool ok = true;
-    for (; __all_sync(0xffffffffu, seg_wait(sg)); ++sg) {
-      const Seg g = seg_at(sg);
-      __syncwarp();
-      if (lane == 0) seg_done(sg);
-      const int n = g.i1 - g.i0;
-      if (!warp_wait(bar(QEMPTY), (sg & 1) ^ 1, abort_flag, p.ctl)) break;
-      // a slot's T tokens x G heads as one box per 64 elements; tokens past the
-      // unit's belong to others and stay in their own rows of S
-      if (lane == 0) {
-        if (sg == 0) fence_proxy_async_smem();  // the plan's words lay where the rows go
-        const int slots = g.split ? 1 : 2, toks = LIST ? 1 : p.T;
-        mbar_arrive_expect_tx(bar(QFULL), slots * L::CH * toks * p.G * 128);
-        for (int i = 0; i < slots; ++i)
-#pragma unroll
-          for (int c = 0; c < L::CH; ++c)
-            tma_load_3d(sQ + i * L::QTILE + c * L::CHUNK, &qmap, bar(QFULL), c * 64, g.j * p.G,
-                        g.tb + i * p.T);
-      }
-      __syncwarp();
-      const int key0 = g.key0(g.i1 - 1, 7);
-      if (!LIST && g.len > key0 && g.len < key0 + kTile) {
-        // the last tile's value rows past the end of the sequence
-        const uint32_t e = ring + 2 * n - 1, stage = e % ST;  // the segment's last entry
-        ok = warp_wait(bar(VTAIL), tails & 1, abort_flag, p.ctl) &&
-             warp_wait(bar(FULL + stage), (e / ST) & 1, abort_flag, p.ctl);
-        if (!ok) break;
-        ++tails;
-        const int first = g.len - key0;
-        for (int x = lane; x < (kTile - first) * 8 * L::CH; x += 32) {
-          const int c = x / ((kTile - first) * 8), o = x % ((kTile - first) * 8);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                           sKV + stage * L::TILE + c * L::CHUNK + first * 128 + o * 16),
-                       "r"(0)
-                       : "memory");
-        }
-        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(VREADY));
+        const int key0 = g.key0(g.i1 - 1, 7);
+        if (!LIST && g.len > key0 && g.len < key0 + kTile) {
+          // the last tile's value rows past the end of the sequence
+          const uint32_t e = ring + 2 * n - 1, stage = e % ST;  // the segment's last entry
+          ok = warp_wait(bar(VTAIL), tails & 1, abort_flag, p.ctl) &&
+               warp_wait(bar(FULL + stage), (e / ST) & 1, abort_flag, p.ctl);
+          if (!ok) break;
+          ++tails;
+          const int first = g.len - key0;
+          for (int x = lane; x < (kTile - first) * 8 * L::CH; x += 32) {
+            const int c = x / ((kTile - first) * 8), o = x % ((kTile - first) * 8);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             sKV + stage * L::TILE + c * L::CHUNK + first * 128 + o * 16),
+                         "r"(0)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(VREADY));
+        }
+        ring += 2 * n;
       }
-      ring += 2 * n;
     }
-  }
   } else if (warp < 12) {
     // ------------------------------------------------------------ softmax and output
     if constexpr (LIST) reg_inc<192>(); else reg_inc<216>();
@@ -528,7 +538,7 @@ attend_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ 
 #pragma unroll
           for (int q = 0; q < 4; ++q) w[q] = low_bits(lim - 32 * q);
           if (p.window) {
-            const int lo = static_cast<int>(max(static_cast<int64_t>(lim) - p.window, static_cast<int64_t>(0)));
+            const int lo = max(lim, p.window) - p.window;
             const int sk = max(p.sinks - key0, 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) w[q] &= ~low_bits(lo - 32 * q) | low_bits(sk - 32 * q);
@@ -826,7 +836,8 @@ size_t attend_workspace(int d) { return AttWs(d).total; }
 cudaError_t launch_attend(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
   // at most 16 rows a unit, on average: a warp each (see attend_rows.cu)
   const int G = a.H / a.Hkv;
-  if (G <= kRowHeads && (a.idx || static_cast<int64_t>(a.n_tok) * G <= static_cast<int64_t>(kRowHeads) * a.n_seq))
+  const bool few = static_cast<int64_t>(a.n_tok) * G <= static_cast<int64_t>(kRowHeads) * a.n_seq;
+  if (G <= kRowHeads && (a.idx || few))
     return launch_attend_rows(a, ctl, s);
   const int64_t tiles = a.idx ? static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kTile - 1) / kTile)
                               : att_ctas();

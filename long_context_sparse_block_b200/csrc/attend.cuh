@@ -488,7 +488,8 @@ __device__ __forceinline__ void write_head(const AttParams& p, const Start& st, 
         cost = cost_of(p, s, end.m);
       }
       if (there)
-        open = make_int4(1, tok, toks | end.j << 16, last_worker(p, st.workers, st.total, st.x1 - end.off + cost));
+        open = make_int4(1, tok, toks | end.j << 16,
+                         last_worker(p, st.workers, st.total, st.x1 - end.off + cost));
     }
   }
   p.head[2 * c] = cont;

@@ -1,17 +1,20 @@
-// Attention over selected tokens for at most 16 query heads per key head.
+// Attention of units of at most 16 rows: selected tokens with at most 16 query heads
+// per key head, and steps of one or a few new tokens over everything they see.
 //
-// The same sums as attend.cu's list form (o = sum over the list of softmax
-// weights times values, one pass with a running reference).  With few heads per
-// gathered row the work is the gather: 4 D bytes per listed token and key head
-// against 4 D G flops, read from L2 as the lists of many rows overlap.  A
-// 128-row tcgen05 tile would hold G live rows, and its long per-tile chain (one
-// live warp of four) takes 2 us for 128 tokens; here a warp owns a (row, key
-// head) unit by itself, m16n8k16 products with the G heads as the 16 rows, and
-// eight such warps on an SM hide each other's latencies.  (1055 rows of 333
-// tokens, 24 heads of 64 over 4 key heads: 173 us with the tcgen05 tile.)
+// The same sums as attend.cu's (one pass with a running reference), over each row's
+// list, or over everything that the 16 / G tokens of a unit see.  With few rows per
+// key head the work is the stream of keys and values: 4 D bytes per token and key
+// head against 4 D flops a row, from L2 for lists (those of many rows overlap), from
+// HBM for the dense form.  A 128-row tcgen05 tile would hold 16 live rows or fewer:
+// its chain (one live warp of four) takes 2 us for 128 tokens, and its idle rows
+// cost power (64 sequences of up to 32768 keys, back to back for a second: clocks
+// fell to 1.2 GHz and a step took 877 us).  Here a warp owns a unit by itself,
+// m16n8k16 products with its rows as the 16, and eight such warps on an SM hide each
+// other's latencies: 730 us there (6.6 TB/s), and for 1055 rows of 333 tokens, 24
+// heads of 64 on 4 key heads, 75 against 173 us.
 //
 // A warp keeps a ring of entries in shared memory, each the key rows or the
-// value rows of 32 tokens, filled by cp.async with the lanes of a row's 16-byte
+// value rows of 16 or 32 tokens, filled by cp.async with the lanes of a row's 16-byte
 // units side by side; it copies ahead over the units' ends, token ids two groups
 // and table entries one group ahead of the copies.  No warp waits for another.
 // The units' groups are laid on a line that is cut evenly over all warps; parts
@@ -27,10 +30,10 @@ constexpr int kWarps = 8;
 constexpr int kGroup = 32;  // tokens summed at a time
 
 // Ring entries hold 32 tokens' rows in the list form, whose rows come from L2 and
-// which is bound by its instructions (256 rows against 320 us with 16 tokens an entry
-// on 512 rows of 1024 tokens, 8 groups of 8 heads), and 16 in the dense form, which
-// streams from HBM and wants its bytes in flight (5/6 of the ring instead of 2/3:
-// 64 sequences of up to 32768 keys 709 against 781 us).
+// which is bound by its instructions (282 us against 320 with 16 tokens an entry on
+// 512 rows of 1024 tokens, 64 heads on 8 key heads), and 16 in the dense form, which
+// streams from HBM and wants its bytes in flight (5/6 of the ring instead of 2/3: 64
+// sequences of up to 32768 keys 709 against 781 us, sustained).
 template <int D, bool LIST>
 struct RowLayout {
   static constexpr int PARTS = LIST ? 1 : 2;  // entries of a group's keys
@@ -67,6 +70,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// List form: short lists (8 groups at most) and many units are left whole, and
+// nothing has to be joined.
+__host__ __device__ inline bool rows_whole(const AttParams& p) {
+  return p.k <= 8 * kGroup || static_cast<int64_t>(p.n_tok) * p.Hkv >= static_cast<int64_t>(8) * p.workers;
+}
+
 template <int D, bool LIST>
 __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p) {
   using L = RowLayout<D, LIST>;
@@ -84,7 +93,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
   {
     Start st;
     if constexpr (LIST) {
-      st = list_start(p, worker, 1);
+      st = list_start(p, worker, rows_whole(p) ? list_tiles(p) : 1);
     } else {
       auto& ps = *reinterpret_cast<PlanShared<2 * kWarps>*>(smem_rows);  // before the first copies
       plan_points<kWarps * 32>(p, ps, [&](int i) {
@@ -398,7 +407,7 @@ cudaError_t launch_rows(const AttParams& p, cudaStream_t s) {
   }
   kern<<<att_ctas(), kWarps * 32, L::BYTES, s>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.workers == 1) return e;
+  if (e != cudaSuccess || p.workers == 1 || (LIST && rows_whole(p))) return e;
   return launch_join<D>(p, kRowHeads, 4, s);
 }
 
@@ -408,11 +417,15 @@ cudaError_t launch_attend_rows(const AttendLaunch& a, const DevCtl& ctl, cudaStr
   // at least 4 groups a worker: below that a unit falls into so many parts that
   // joining them costs more than the shorter stretches save (8 rows of 2048 tokens,
   // 16 heads: 47 us with one group a worker, 18 us with four).  The dense form finds
-  // its groups on the device.
+  // its groups on the device; it has at most 96 workers a unit (one token over 32768
+  // keys, 32 heads on 8: 43 us, with 48 52, with all 148 47).
   int64_t workers = static_cast<int64_t>(att_ctas()) * kWarps;
   if (a.idx) {
     const int64_t groups = static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kGroup - 1) / kGroup);
-    workers = std::min(workers, std::max<int64_t>(1, groups / 4));
+    workers = std::min(workers, a.k <= 8 * kGroup ? static_cast<int64_t>(a.n_tok) * a.Hkv
+                                                  : std::max<int64_t>(1, groups / 4));
+  } else {
+    workers = std::min(workers, static_cast<int64_t>(96) * a.n_tok * a.Hkv);
   }
   const AttParams p = att_params(a, ctl, static_cast<int>(workers), true);
   if (a.idx) return a.d == 128 ? launch_rows<128, true>(p, s) : launch_rows<64, true>(p, s);
