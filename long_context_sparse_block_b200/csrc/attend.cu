@@ -40,7 +40,7 @@
 // heads: 834 us = 1278 TFLOP/s, 76 % of the measured bf16 rate; sustained for a
 // second, under the power cap, 957 us (80 % of the sustained rate).  A step (one
 // tile for both slots) takes 1.95 us: 2048 cycles of products and as many of the
-// special-function unit, half busy each, behind the chain S, maximum, exponentials,
+// special-function unit, 63 % busy each, along the chain S, maximum, exponentials,
 // P V of a slot.  Exponentials on the FMA pipe instead (degree 5, 3, 5 or 8 of 16)
 // measured 880, 899 and 967 against 853 us: issue slots, not that unit, are short.
 // The list form gathers 4096 lists of 2048 tokens (64 heads on one key head) in 570
