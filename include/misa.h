@@ -433,7 +433,7 @@ int misa_rope_frequencies(int rope_dim, double base, int scaling, double factor,
  *   lse[t, h] = log sum_s exp(scale * Q[t, h] . K[s, h / G])   (nullable, fp32)
  *   Q, out [n_tok, H, d] bf16; k_pages, v_pages [n_pages, page_size, H_kv, d] bf16;
  *   block_tables [n_seq, max_blocks], cu_q [n_seq + 1], seq_lens [n_seq] int32
- *   (device); d in {64, 128}, H_kv divides H, G <= 128, page_size 16, 32, 64 or
+ *   (device); d in {64, 128}, H_kv <= 8192 divides H, G <= 128, page_size 16, 32, 64 or
  *   128 (else MISA_ERR_UNSUPPORTED); scale > 0; sinks need a window.  Entries of
  *   cu_q ascend; those past n_tok are taken as n_tok.
  * One call serves prefill chunks, single new tokens and mixed batches; rows past

@@ -167,7 +167,8 @@ int check_attend(AttendLaunch& a, const uint16_t* Q, const uint16_t* k_pages,
       !(scale > 0.0f) || !std::isfinite(scale))
     return MISA_ERR_INVALID_ARG;
   const int shift = page_shift_of(page_size);
-  if (shift < 0 || (d != 64 && d != 128) || H / H_kv > 128) return MISA_ERR_UNSUPPORTED;
+  if (shift < 0 || (d != 64 && d != 128) || H / H_kv > 128 || H_kv > 8192)
+    return MISA_ERR_UNSUPPORTED;
   if (n_pages < 1 || n_pages > (0x7fffffffLL >> shift)) return MISA_ERR_INVALID_ARG;
   a.Q = Q;
   a.k_pages = k_pages;

@@ -248,6 +248,45 @@ def test_selected_of_everything_equals_attend(lib):
         check_rows(o, l, rows, Q, cache, seqs, lambda t: slice(0, pos[t] + 1), 8, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("H,n", [(16, 1), (16, 40), (512, 2)])
+def test_rows_past_2_31_elements_of_a_pool(lib, H, n):
+    # pools of 16416 pages x 64 rows x 16 heads x 128 (2.15e9 elements each): the sequence
+    # lies in the last pages, and is written there by the append
+    Hkv, d, page, n_pages, length = 16, 128, 64, 16416, 190
+    kp = torch.empty((n_pages, page, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    vp = torch.empty_like(kp)
+    table = torch.tensor([[n_pages - 1, n_pages - 3, n_pages - 2]], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn((length, Hkv, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32, device="cuda")
+    plan = lib.misa_plan_step(i32([length]), i32([0]), table, page, n_tok=length, n_pages=n_pages)
+    f, _ = lib.misa_rope_frequencies(16)
+    lib.misa_cache_append(k.cuda(), i32(np.zeros(length)), plan.slots, f, kp, v=v.cuda(), v_pages=vp)
+    Q = torch.randn((n, H, d), generator=g).to(torch.bfloat16).cuda()
+
+    class Plain:                                  # position 0: the rows as they were
+        K, V = [k], [v]
+    pos = np.arange(length - n, length)
+    out, lse = lib.misa_attend_paged(Q, kp, vp, table, i32([0, n]), i32([length]), want_lse=True)
+    rows = _sample(n, 3)
+    seqs = np.zeros(n, dtype=int)
+    check_rows(out[:, ::37], lse[:, ::37], rows, Q[:, ::37], _Every(Plain, 37, H // Hkv), seqs,
+               lambda t: slice(0, pos[t] + 1), 1, d ** -0.5)
+    idx = i32(np.tile(np.arange(0, length, 3), (n, 1)))
+    out, lse = lib.misa_attend_selected(Q, kp, vp, table, i32(seqs), i32(pos), idx, want_lse=True)
+    check_rows(out[:, ::37], lse[:, ::37], rows, Q[:, ::37], _Every(Plain, 37, H // Hkv), seqs,
+               lambda t: np.array([x for x in range(0, length, 3) if x <= pos[t]]), 1, d ** -0.5)
+    assert lib.misa_last_device_status() == lib.MISA_OK
+
+
+class _Every:
+    """A cache seen from every step-th query head: one key head for each."""
+
+    def __init__(self, cache, step, G):
+        pick = lambda x: x[:, [h // G for h in range(0, x.shape[1] * G, step)]]
+        self.K, self.V = [pick(x) for x in cache.K], [pick(x) for x in cache.V]
+
+
 # ------------------------------------------------------------------ streams, graphs, waits
 
 def test_attend_in_a_graph_and_beside_another_stream(lib):

@@ -77,7 +77,7 @@ def test_attend_refusals(lib):
         ("inv", dict(q=None)), ("inv", dict(q=ODD)), ("inv", dict(kp=None)), ("inv", dict(vp=ODD)),
         ("inv", dict(bt=None)), ("inv", dict(mb=0)), ("uns", dict(ps=8)), ("inv", dict(np=0)),
         ("inv", dict(np=1 << 60)), ("inv", dict(n=-1)), ("inv", dict(nt=-1)), ("inv", dict(H=0)),
-        ("inv", dict(Hk=3)), ("uns", dict(H=1032)), ("uns", dict(d=32)), ("uns", dict(d=96)),
+        ("inv", dict(Hk=3)), ("uns", dict(H=1032)), ("uns", dict(H=8193, Hk=8193)), ("uns", dict(d=32)), ("uns", dict(d=96)),
         ("inv", dict(sc=0.0)), ("inv", dict(sc=float("inf"))), ("inv", dict(sc=float("nan"))),
         ("inv", dict(o=None)), ("inv", dict(l=ODD)), (0, dict(nt=0)), (0, dict(n=0)),
         (lib.MISA_ERR_WORKSPACE, dict(ws=None)), (lib.MISA_ERR_WORKSPACE, dict(wb=1000)),
