@@ -78,9 +78,10 @@ struct AttLayout {
   static_assert(ALLOC <= 232448, "shared memory of an SM");
 };
 
-// List form: with 8 units or more for a CTA, or units of one or two tiles, units are
-// left whole (the CTAs' work then differs by one unit at most) and nothing has to be
-// joined.
+// List form: units are left whole, and nothing has to be joined, with 8 of them or
+// more for a CTA, or with lists of at most two tiles (the CTAs' work then differs by
+// one unit, 5 us for two tiles, less than joining takes: 900 units of 250 tokens 33
+// against 42 us).
 __host__ __device__ inline bool whole_units(const AttParams& p, int ctas) {
   return p.k <= 2 * kTile || static_cast<int64_t>(p.n_tok) * p.Hkv >= static_cast<int64_t>(8) * ctas;
 }

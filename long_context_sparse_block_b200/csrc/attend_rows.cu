@@ -11,7 +11,7 @@
 // fell to 1.2 GHz and a step took 877 us).  Here a warp owns a unit by itself,
 // m16n8k16 products with its rows as the 16, and eight such warps on an SM hide each
 // other's latencies: 730 us there (6.6 TB/s), and for 1055 rows of 333 tokens, 24
-// heads of 64 on 4 key heads, 75 against 173 us.
+// heads of 64 on 4 key heads, 78 against 173 us.
 //
 // A warp keeps a ring of entries in shared memory, each the key rows or the
 // value rows of 16 or 32 tokens, filled by cp.async with the lanes of a row's 16-byte
@@ -70,10 +70,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// List form: short lists (8 groups at most) and many units are left whole, and
-// nothing has to be joined.
+// List form: units are left whole, and nothing has to be joined, where there are many,
+// where lists are short (4 groups), or of up to 8 groups with a worker for each
+// (2400 units of 7 groups for 1184 workers: 36 us cut, 39 whole).
 __host__ __device__ inline bool rows_whole(const AttParams& p) {
-  return p.k <= 8 * kGroup || static_cast<int64_t>(p.n_tok) * p.Hkv >= static_cast<int64_t>(8) * p.workers;
+  const int64_t units = static_cast<int64_t>(p.n_tok) * p.Hkv;
+  return units >= static_cast<int64_t>(8) * p.workers || p.k <= 4 * kGroup ||
+         (p.k <= 8 * kGroup && units <= p.workers);
 }
 
 template <int D, bool LIST>
@@ -110,7 +113,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
   // (b), copies (c).  The segments it meets go to the ring `segs` for the sums.
   const int64_t cap = static_cast<int64_t>(p.max_blocks) << p.page_shift;
   struct Ahead {
-    int s, pg, j, live;
+    int s, lim, pg, j, live;
     const int32_t* bt;
   };
   Seg as;  // the segment whose groups are being read
@@ -122,6 +125,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
   auto read_ids = [&](Ahead& a) {
     a.live = 0;
     a.s = -1;
+    a.lim = -1;
     a.j = 0;
     a.bt = p.bts;
     if (!ended && ai >= as.i1) {
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
     if (ended) return;
     if constexpr (LIST) {
       if (ai * kGroup + lane < p.k) a.s = __ldg(alist + ai * kGroup);
-      if (a.s > as.p0) a.s = -1;
+      a.lim = as.p0;  // (compared one step later: the id is still on its way)
     } else {
       a.s = as.key0(ai, 5) + lane;
       if (a.s >= as.len) a.s = -1;  // rows past the sequence: zeros, whatever the cache holds
@@ -149,6 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
     ++ai;
   };
   auto read_page = [&](Ahead& a) {
+    if (LIST && a.s > a.lim) a.s = -1;
     if (LIST && a.s >= cap) {
       report(p.ctl, DEV_BAD_INPUT);
       a.s = -1;
@@ -157,6 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
   };
   Ahead a0, a1, a2;  // copies next, table entry read, ids read
   a0.s = a1.s = a2.s = -1;
+  a0.lim = a1.lim = a2.lim = -1;
   a0.live = a1.live = a2.live = 0;
   a0.j = a1.j = a2.j = 0;
   auto read_on = [&]() {
@@ -414,7 +420,7 @@ cudaError_t launch_rows(const AttParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attend_rows(const AttendLaunch& a, const DevCtl& ctl, cudaStream_t s) {
-  // at least 4 groups a worker: below that a unit falls into so many parts that
+  // at least 4 groups a worker (or a unit): below that a unit falls into so many parts that
   // joining them costs more than the shorter stretches save (8 rows of 2048 tokens,
   // 16 heads: 47 us with one group a worker, 18 us with four).  The dense form finds
   // its groups on the device; it has at most 96 workers a unit (one token over 32768
@@ -422,8 +428,9 @@ cudaError_t launch_attend_rows(const AttendLaunch& a, const DevCtl& ctl, cudaStr
   int64_t workers = static_cast<int64_t>(att_ctas()) * kWarps;
   if (a.idx) {
     const int64_t groups = static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kGroup - 1) / kGroup);
-    workers = std::min(workers, a.k <= 8 * kGroup ? static_cast<int64_t>(a.n_tok) * a.Hkv
-                                                  : std::max<int64_t>(1, groups / 4));
+    const int64_t units = static_cast<int64_t>(a.n_tok) * a.Hkv;
+    workers = a.k <= 8 * kGroup && units <= workers ? units
+                                                    : std::min(workers, std::max(units, groups / 4));
   } else {
     workers = std::min(workers, static_cast<int64_t>(96) * a.n_tok * a.Hkv);
   }
