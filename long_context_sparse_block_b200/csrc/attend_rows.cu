@@ -235,21 +235,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
     uint32_t q[D / 16][4];
     float o[D / 8][4];
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-    int64_t orow[2];  // rows g and g + 8 of the results
-    int pos[2];
+    // row of the results of the unit's row r (worked out again where it is needed:
+    // registers are short in between)
+    auto row_at = [&](int r) {
+      const int tok = r * p.g_inv >> 16;
+      return static_cast<int64_t>(seg.tb + tok) * p.H + seg.j * p.G + r - tok * p.G;
+    };
+    {
+      const uint16_t* qr[2] = {p.Q + row_at(g) * D + 2 * c, p.Q + row_at(g + 8) * D + 2 * c};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = g + 8 * h, tok = r * p.g_inv >> 16;
-      orow[h] = static_cast<int64_t>(seg.tb + tok) * p.H + seg.j * p.G + r - tok * p.G;
-      pos[h] = seg.p0 + tok;
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          q[kk][x] = g + 8 * (x & 1) < rows ? __ldg(reinterpret_cast<const uint32_t*>(
+                                                  qr[x & 1] + kk * 16 + 8 * (x >> 1)))
+                                            : 0u;
     }
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        q[kk][x] = g + 8 * (x & 1) < rows ? __ldg(reinterpret_cast<const uint32_t*>(
-                                                p.Q + orow[x & 1] * D + kk * 16 + 8 * (x >> 1) + 2 * c))
-                                          : 0u;
 #pragma unroll
     for (int x = 0; x < D / 8; ++x)
 #pragma unroll
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
       } else {
         // groups that every row sees need no test
         const int key0 = seg.key0(i, 5);
+        const int pos[2] = {seg.p0 + (g * p.g_inv >> 16), seg.p0 + ((g + 8) * p.g_inv >> 16)};
         if (key0 + kGroup - 1 > seg.p0 ||
             (p.window && key0 <= seg.p0 + seg.toks - 1 - p.window && key0 + kGroup > p.sinks)) {
 #pragma unroll
@@ -387,11 +389,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) rows_kernel(const AttParams p)
               make_float2(o[x][2 * h], o[x][2 * h + 1]);
       } else {
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t orow = row_at(r);
 #pragma unroll
         for (int x = 0; x < D / 8; ++x)
-          *reinterpret_cast<uint32_t*>(p.out + orow[h] * D + x * 8 + 2 * c) =
+          *reinterpret_cast<uint32_t*>(p.out + orow * D + x * 8 + 2 * c) =
               bf16x2(o[x][2 * h] * inv, o[x][2 * h + 1] * inv);
-        if (p.lse && c == 0) p.lse[orow[h]] = row_lse(m[h], sum);
+        if (p.lse && c == 0) p.lse[orow] = row_lse(m[h], sum);
       }
     }
   }
