@@ -684,9 +684,9 @@ def misa_rope_fp8(x, positions, inv_freq, offset: int = 0, interleaved: bool = F
         raise ValueError("x must be [n, H, d]")
     dev, (n, H, d) = x.get_device(), x.shape
     if codes is None:
-        codes = torch.empty((n, H, d), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((n, H, d), dtype=torch.uint8)
     if scale is None:
-        scale = torch.empty((n, H), dtype=torch.float32, device=x.device)
+        scale = x.new_empty((n, H), dtype=torch.float32)
     if n == 0:
         return codes, scale
     a = _rope_args(x, positions, inv_freq, offset, interleaved, amplitude, dev, d)

@@ -160,6 +160,25 @@ def test_attend_reports_bad_pages_and_lengths(lib):
     check_rows(out, None, [0], Q, cache, seqs, lambda t: slice(0, 100), 4, 64 ** -0.5)
 
 
+def test_bf16_codes_as_integers_and_default_buffers(lib):
+    # the binding takes bf16 codes in 16-bit integer tensors too, and makes its buffers
+    cache, Q, cu, ln, seqs, pos = _batch([1, 3], [50, 200], 8, 2, 64, 32, seed=49)
+    ref, rlse = _run(lib, cache, Q, cu, ln)
+    i16 = lambda t: t.view(torch.int16)
+    out, lse = lib.misa_attend_paged(i16(Q), i16(cache.k_pages), i16(cache.v_pages), cache.table, cu, ln,
+                                     want_lse=True)
+    assert out.dtype == torch.int16 and torch.equal(out.view(torch.bfloat16), ref)
+    assert torch.equal(lse, rlse)
+    again, none = lib.misa_attend_paged(Q, cache.k_pages, cache.v_pages, cache.table, cu, ln)
+    assert none is None and torch.equal(again, ref)
+    with pytest.raises(ValueError, match="ws holds"):
+        lib.misa_attend_paged(Q, cache.k_pages, cache.v_pages, cache.table, cu, ln,
+                              ws=torch.empty(1000, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        lib.misa_attend_paged(Q.transpose(0, 1).contiguous().transpose(0, 1), cache.k_pages,
+                              cache.v_pages, cache.table, cu, ln)
+
+
 # ------------------------------------------------------------------ selected tokens
 
 def _lists(pos, k, seed, shuffle=False):
