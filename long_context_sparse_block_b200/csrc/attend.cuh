@@ -42,6 +42,7 @@ struct AttParams {
   int tile_sh;              // log2 of a tile's keys: 7 (row kernel: 5)
   int unit_cost;            // what a unit costs beside its keys, in keys
   int least_sh;             // log2 of the keys that a worker's stretch is worth at least
+  int few;                  // workers that cheap joining allows (see plan_points)
   int g_inv;                // 65536 / G + 1: x / G == x * g_inv >> 16 for x < 384, G <= 128
   int window;               // 0: none
   int sinks;
@@ -354,8 +355,12 @@ __device__ __forceinline__ void plan_points(const AttParams& p, PlanShared<NP>& 
     }
   }
   const int64_t all = total;
-  const int workers =
-      static_cast<int>(min(static_cast<int64_t>(p.workers), max(all >> p.least_sh, int64_t{1})));
+  // Workers: a stretch is worth 2^least_sh keys at least, and few of them share a unit
+  // (their parts have to be joined) unless it is long: then half of all, with four
+  // times the stretch (one token over a million keys: 0.18 ms, with 96 0.59).
+  int64_t want = min(all >> p.least_sh, static_cast<int64_t>(p.few));
+  want = max(want, min(all >> (p.least_sh + 2), static_cast<int64_t>(p.workers / 2)));
+  const int workers = static_cast<int>(max(min(want, static_cast<int64_t>(p.workers)), int64_t{1}));
   if (tid < NP) ps.x[tid] = cut(p, workers, all, min(index(tid), workers));
   if (tid == 0) {
     ps.total = all;
@@ -693,6 +698,8 @@ inline AttParams att_params(const AttendLaunch& a, const DevCtl& ctl, int worker
   p.tile_sh = rows ? 5 : 7;
   p.unit_cost = rows ? 128 : 4 * kTile;
   p.least_sh = rows ? 7 : 8;
+  // (row kernel: 96 a unit of at most n_tok x H_kv)
+  p.few = rows ? static_cast<int>(std::min<int64_t>(workers, int64_t{96} * a.n_tok * a.Hkv)) : workers;
   p.workers = workers;
   p.w_inv = workers > 1 ? ~uint64_t{0} / static_cast<uint64_t>(workers) + 1 : 0;
   p.g_inv = 65536 / p.G + 1;

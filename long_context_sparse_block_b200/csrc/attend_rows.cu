@@ -426,16 +426,14 @@ cudaError_t launch_attend_rows(const AttendLaunch& a, const DevCtl& ctl, cudaStr
   // at least 4 groups a worker (or a unit): below that a unit falls into so many parts that
   // joining them costs more than the shorter stretches save (8 rows of 2048 tokens,
   // 16 heads: 47 us with one group a worker, 18 us with four).  The dense form finds
-  // its groups on the device; it has at most 96 workers a unit (one token over 32768
-  // keys, 32 heads on 8: 43 us, with 48 52, with all 148 47).
+  // its groups on the device; short ones have at most 96 workers a unit (one token over
+  // 32768 keys, 32 heads on 8: 43 us, with 48 52, with all 148 47).
   int64_t workers = static_cast<int64_t>(att_ctas()) * kWarps;
   if (a.idx) {
     const int64_t groups = static_cast<int64_t>(a.n_tok) * a.Hkv * ((a.k + kGroup - 1) / kGroup);
     const int64_t units = static_cast<int64_t>(a.n_tok) * a.Hkv;
     workers = a.k <= 8 * kGroup && units <= workers ? units
                                                     : std::min(workers, std::max(units, groups / 4));
-  } else {
-    workers = std::min(workers, static_cast<int64_t>(96) * a.n_tok * a.Hkv);
   }
   const AttParams p = att_params(a, ctl, static_cast<int>(workers), true);
   if (a.idx) return a.d == 128 ? launch_rows<128, true>(p, s) : launch_rows<64, true>(p, s);
